@@ -21,6 +21,8 @@ import math
 
 from . import _capi
 from ._capi import GqaError, STATUS, STATUS_CODE, strerror
+from .kv8 import (KvTables, gqa_attn_kv8_append, gqa_attn_kv8_decode, gqa_attn_kv8_gather,
+                  gqa_attn_kv_tables)
 
 __all__ = ["gqa_attn", "gqa_attn_host", "gqa_attn_kvcache", "gqa_attn_blocksparse",
            "gqa_attn_backward",
@@ -28,7 +30,9 @@ __all__ = ["gqa_attn", "gqa_attn_host", "gqa_attn_kvcache", "gqa_attn_blockspars
            "gqa_attn_workspace_bytes", "gqa_attn_set_workspace", "gqa_attn_get_device_error",
            "GqaError", "STATUS", "STATUS_CODE", "strerror", "library_path",
            "gqa_attn_blocksparse_varlen", "gqa_attn_blocksparse_varlen_plan",
-           "SparseVarlenPlan", "gqa_attn_fp8"]
+           "SparseVarlenPlan", "gqa_attn_fp8",
+           "KvTables", "gqa_attn_kv_tables", "gqa_attn_kv8_append", "gqa_attn_kv8_gather",
+           "gqa_attn_kv8_decode"]
 
 KERNEL_NAMES = {0: "none", 1: "prefill_sm100", 2: "decode_splitkv", 3: "zero_fill"}
 

@@ -33,6 +33,11 @@ EXPORTS = (
     "gqa_attn_decode_fp8",
     "gqa_attn_selftest_timeout",
     "gqa_attn_fwd_window",
+    "gqa_attn_kv_tables",
+    "gqa_attn_kv8_append",
+    "gqa_attn_kv8_gather",
+    "gqa_attn_kv8_decode_workspace_bytes",
+    "gqa_attn_kv8_decode",
 )
 
 STATUS = {
@@ -106,6 +111,17 @@ def load() -> ctypes.CDLL:
     lib.gqa_attn_decode_fp8.restype = I
     lib.gqa_attn_selftest_timeout.argtypes = [I, P]
     lib.gqa_attn_selftest_timeout.restype = I
+    LL = ctypes.c_longlong
+    lib.gqa_attn_kv_tables.argtypes = [P] * 10 + [I] * 5 + [P]
+    lib.gqa_attn_kv_tables.restype = I
+    lib.gqa_attn_kv8_append.argtypes = [P] * 7 + [I, I, I, LL, LL, I, I, I, P]
+    lib.gqa_attn_kv8_append.restype = I
+    lib.gqa_attn_kv8_gather.argtypes = [P] * 8 + [I] * 8 + [P]
+    lib.gqa_attn_kv8_gather.restype = I
+    lib.gqa_attn_kv8_decode_workspace_bytes.argtypes = [I] * 5
+    lib.gqa_attn_kv8_decode_workspace_bytes.restype = Z
+    lib.gqa_attn_kv8_decode.argtypes = [P] * 11 + [Z] + [I] * 10 + [F, I, P]
+    lib.gqa_attn_kv8_decode.restype = I
     lib.gqa_attn_strerror.argtypes = [I]
     lib.gqa_attn_strerror.restype = ctypes.c_char_p
     _lib = lib

@@ -14,7 +14,7 @@ import sys
 
 HERE = pathlib.Path(__file__).resolve().parent
 ROOT = HERE.parent
-SRC = HERE / "csrc" / "gqa_attn.cu"
+SRC = HERE / "csrc" / "library.cu"
 OUT = HERE / "libgqa_attn.so"
 DEPS = sorted((HERE / "csrc").glob("*.cu*")) + [ROOT / "include" / "gqa_attn.h"]
 

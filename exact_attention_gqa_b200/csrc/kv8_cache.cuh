@@ -1,0 +1,348 @@
+// The 8-bit paged KV cache with a scale for each block of tokens and head: its tables,
+// its writer and its reader back to bf16 (the attention over it is kv8_decode.cuh).
+//
+// A stored value is code * scale, the code in e4m3 and the scale a power of two.  A power
+// of two loses nothing against a free scale, because e4m3 is a floating-point format: its
+// relative step does not depend on where in its range a value lies.  What it gains: x / s
+// is exact, so a code is x rounded once, and when a block's scale grows by 2^n its codes
+// are divided by 2^n exactly, apart from the bits that fall below the subnormal step.  So
+// tokens can be written one at a time into a block without their error adding up.
+#pragma once
+#include "decode.cuh"
+
+namespace gqa {
+
+constexpr int kDevNoPages = 4;  // the free pages ran out, or a row of the block table did
+
+struct KvTablesParams {
+    const int* cached_lens;  // [B]
+    const int* new_lens;     // [B]
+    const int* free_pages;   // [n_free]
+    const int* free_start;   // [1] or null (0)
+    int* block_table;        // [B, max_pages]
+    int* slot_map;           // [max_tokens]
+    int* seqlens_k;          // [B]
+    int* cu_seqlens_q;       // [B + 1]
+    int* cu_seqlens_k;       // [B + 1]
+    int* free_end;           // [1]
+    int B, n_free, max_pages, page_shift, max_tokens;
+};
+
+__device__ __forceinline__ int sat_i32(long long x) {
+    return x > INT32_MAX ? INT32_MAX : int(x);
+}
+
+// Index of the last entry of the non-decreasing cu[0..n] that is <= x, below n (0 <= x <
+// cu[n]): the sequence that owns packed row x.
+template <typename Ptr>
+__device__ __forceinline__ int owner_of(Ptr cu, int n, int x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cu[mid] <= x)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
+}
+
+// Block table rows, slot map and prefix sums from the request lengths.  Every CTA repeats
+// the scan over the B requests (two loads and a block scan, so no CTA waits for another
+// and one launch does it all) and then takes its share of the slots and of the pages.
+constexpr int kTablesThreads = 512;
+__global__ void __launch_bounds__(kTablesThreads) kv_tables(const KvTablesParams p) {
+    extern __shared__ int sm_tables[];
+    int* cu_q = sm_tables;          // [B + 1] new tokens before request b
+    int* pg = sm_tables + p.B + 1;  // [B + 1] new pages before request b
+    __shared__ long long warp_sum[3][kTablesThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ps = 1 << p.page_shift;
+    const long long cap = (long long)p.max_pages << p.page_shift;
+    const int per = (p.B + kTablesThreads - 1) / kTablesThreads;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    auto lengths = [&](int b, int& had, int& add) {
+        had = p.cached_lens[b];
+        add = p.new_lens[b];
+        if (had < 0 || add < 0 || (long long)had + add > cap) {
+            raise_device_error(kDevNoPages);
+            had = int(min((long long)max(had, 0), cap));
+            add = int(min((long long)max(add, 0), cap - had));
+        }
+    };
+    long long sum[3] = {0, 0, 0};  // new tokens, new pages, tokens
+    for (int b = b0; b < b1; ++b) {
+        int had, add;
+        lengths(b, had, add);
+        sum[0] += add;
+        sum[1] += ((long long)had + add + ps - 1) / ps - ((long long)had + ps - 1) / ps;
+        sum[2] += (long long)had + add;
+    }
+    long long inc[3] = {sum[0], sum[1], sum[2]};
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1)
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const long long o = __shfl_up_sync(0xffffffffu, inc[i], off);
+            if (lane >= off) inc[i] += o;
+        }
+    if (lane == 31)
+        for (int i = 0; i < 3; ++i) warp_sum[i][warp] = inc[i];
+    __syncthreads();
+    long long at[3];
+    for (int i = 0; i < 3; ++i) {
+        at[i] = inc[i] - sum[i];
+        for (int w = 0; w < warp; ++w) at[i] += warp_sum[i][w];
+    }
+    const bool first = blockIdx.x == 0;
+    for (int b = b0; b < b1; ++b) {
+        int had, add;
+        lengths(b, had, add);
+        cu_q[b] = sat_i32(at[0]);
+        pg[b] = sat_i32(at[1]);
+        if (first) {
+            p.cu_seqlens_q[b] = sat_i32(at[0]);
+            p.cu_seqlens_k[b] = sat_i32(at[2]);
+            p.seqlens_k[b] = had + add;
+        }
+        at[0] += add;
+        at[1] += ((long long)had + add + ps - 1) / ps - ((long long)had + ps - 1) / ps;
+        at[2] += (long long)had + add;
+    }
+    const int start = p.free_start ? max(*p.free_start, 0) : 0;
+    if (p.B == 0 ? tid == 0 : b0 < p.B && b1 == p.B) {  // the thread with the last request
+        cu_q[p.B] = sat_i32(at[0]);
+        pg[p.B] = sat_i32(at[1]);
+        if (first) {
+            p.cu_seqlens_q[p.B] = sat_i32(at[0]);
+            p.cu_seqlens_k[p.B] = sat_i32(at[2]);
+            *p.free_end = sat_i32(start + at[1]);
+            if (start + at[1] > p.n_free || at[0] > p.max_tokens)
+                raise_device_error(kDevNoPages);
+        }
+    }
+    __syncthreads();
+    const int tokens = cu_q[p.B], pages = pg[p.B];
+    auto free_page = [&](long long f) { return f < p.n_free ? __ldg(p.free_pages + f) : -1; };
+    const int stride = gridDim.x * kTablesThreads;
+    for (int f = blockIdx.x * kTablesThreads + tid; f < pages; f += stride) {
+        const int b = owner_of(pg, p.B, f);
+        int had, add;
+        lengths(b, had, add);
+        p.block_table[size_t(b) * p.max_pages + (had + ps - 1) / ps + (f - pg[b])] =
+            free_page((long long)start + f);
+    }
+    for (int t = blockIdx.x * kTablesThreads + tid; t < p.max_tokens; t += stride) {
+        int slot = -1;
+        if (t < tokens) {
+            const int b = owner_of(cu_q, p.B, t);
+            int had, add;
+            lengths(b, had, add);
+            const int pos = had + (t - cu_q[b]);
+            const int lp = pos >> p.page_shift, lp0 = (had + ps - 1) / ps;
+            // a page of the cached tokens is in the table already; a new one is not read
+            // back from there, because another CTA may be about to write it
+            const int page = lp < lp0 ? p.block_table[size_t(b) * p.max_pages + lp]
+                                      : free_page((long long)start + pg[b] + (lp - lp0));
+            if (page >= 0) slot = int(((long long)page << p.page_shift) + (pos & (ps - 1)));
+        }
+        p.slot_map[t] = slot;
+    }
+}
+
+// ------------------------------------------------------------------------------ append
+struct Kv8AppendParams {
+    struct Side {
+        const __nv_bfloat16* x;  // new keys or values, rows of Hkv * D
+        long long stride;        // elements from one token to the next
+        uint8_t* codes;          // [num_pages * page_size, Hkv, D]
+        float* scale;            // [num_pages * page_size / sb, Hkv]
+    };
+    Side k, v;
+    const int* slot_map;  // [T]
+    int T, Hkv, sb_shift;
+    int slots;  // num_pages * page_size
+};
+
+// The smallest power of two s, at least 2^-126, with a <= 448 s (448 = 1.75 * 2^8); a is
+// finite and >= 0.
+__device__ __forceinline__ float pow2_scale(float a) {
+    const uint32_t u = __float_as_uint(a);
+    const int e = int(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float(uint32_t(max(e, -126) + 127) << 23);
+}
+
+constexpr float kBf16Max = 3.3895313892515355e38f;
+
+// The largest of a and |x| of eight bf16; fmaxf passes over NaN.
+__device__ __forceinline__ float amax8(const uint4& x, float a) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        a = fmaxf(a, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+    return a;
+}
+
+// eight bf16 times inv -> eight e4m3 codes (rounded to nearest even, saturating)
+__device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
+    return make_uint2(
+        pack_e4m3x4(bf16_lo(x.x) * inv, bf16_hi(x.x) * inv, bf16_lo(x.y) * inv,
+                    bf16_hi(x.y) * inv),
+        pack_e4m3x4(bf16_lo(x.z) * inv, bf16_hi(x.z) * inv, bf16_lo(x.w) * inv,
+                    bf16_hi(x.w) * inv));
+}
+
+// four codes -> four fp32 (exact)
+__device__ __forceinline__ void decode4(uint32_t c, float (&f)[4]) {
+    uint32_t lo, hi;
+    e4m3x4_to_f16x4(c, lo, hi);
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(f[0]), "=f"(f[1])
+        : "r"(lo));
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
+        : "=f"(f[2]), "=f"(f[3])
+        : "r"(hi));
+}
+
+// One warp for each (token, head) of K or V (blockIdx.y); only the warp of a run's first
+// token works, for the whole run: the following tokens of the same scale block.
+template <int D>
+__global__ void __launch_bounds__(256) kv8_append(const Kv8AppendParams p) {
+    constexpr int LPR = D / 8;       // lanes of one row, eight elements each
+    constexpr int RPW = 32 / LPR;    // rows a warp handles at a time
+    const int lane = threadIdx.x & 31;
+    const long long job = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int t = int(job / p.Hkv), h = int(job - (long long)t * p.Hkv);
+    if (t >= p.T) return;
+    const int slot = __ldg(p.slot_map + t);
+    if (slot < 0 || slot >= p.slots) {
+        if (lane == 0 && slot != -1) raise_device_error(kDevBadKvIndex);
+        return;
+    }
+    const int blk = slot >> p.sb_shift;
+    auto mine = [&](int i) {  // token i belongs to this block
+        const int s = __ldg(p.slot_map + i);
+        return s >= 0 && s < p.slots && (s >> p.sb_shift) == blk;
+    };
+    if (t > 0 && mine(t - 1)) return;
+    int n = 0;
+    for (bool more = true; more;) {
+        const int i = t + n + lane;
+        const uint32_t in = __ballot_sync(0xffffffffu, i < p.T && mine(i));
+        more = in == 0xffffffffu;
+        n += more ? 32 : __ffs(~in) - 1;
+    }
+    const Kv8AppendParams::Side& io = blockIdx.y == 0 ? p.k : p.v;
+    const int sb = 1 << p.sb_shift;
+    const int r = lane / LPR, c = lane % LPR;
+    const __nv_bfloat16* x = io.x + (long long)t * io.stride + h * D + c * 8;
+    auto load = [&](int i) {
+        return __ldg(reinterpret_cast<const uint4*>(x + (long long)i * io.stride));
+    };
+    float a = 0.f;
+    bool restart = false;
+    for (int i = r; i < n; i += RPW) {
+        a = amax8(load(i), a);
+        restart |= (__ldg(p.slot_map + t + i) & (sb - 1)) == 0;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+    restart = __any_sync(0xffffffffu, restart);
+    float s = pow2_scale(fminf(a, kBf16Max));  // infinity: the largest finite value
+    float* scale = io.scale + (size_t(blk) * p.Hkv + h);
+    uint8_t* base = io.codes + (size_t(blk) << p.sb_shift) * p.Hkv * D + h * D + c * 8;
+    const size_t row = size_t(p.Hkv) * D;
+    if (!restart) {
+        // a scale that no append wrote (not finite, not positive) holds nothing to keep
+        const float s0 = *scale;
+        if (s0 > 0.f && s0 < INFINITY) {
+            const uint32_t u = __float_as_uint(s0);
+            const float up = (u & 0x7fffffu) ? __uint_as_float(((u >> 23) + 1) << 23) : s0;
+            s = fmaxf(s, fminf(fmaxf(up, 1.1754943508222875e-38f), 1.7014118346046923e38f));
+            if (s != s0) {
+                const float f = s0 / s;
+                for (int i = r; i < sb; i += RPW) {
+                    bool now = false;  // written by this call
+                    for (int j = 0; j < n; ++j)
+                        now |= (__ldg(p.slot_map + t + j) & (sb - 1)) == i;
+                    if (now) continue;
+                    uint2* d = reinterpret_cast<uint2*>(base + i * row);
+                    const uint2 o = *d;
+                    float y[4], z[4];
+                    decode4(o.x, y);
+                    decode4(o.y, z);
+                    *d = make_uint2(pack_e4m3x4(y[0] * f, y[1] * f, y[2] * f, y[3] * f),
+                                    pack_e4m3x4(z[0] * f, z[1] * f, z[2] * f, z[3] * f));
+                }
+            }
+        }
+    }
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0) *scale = s;
+    const float inv = 1.f / s;
+    for (int i = r; i < n; i += RPW) {
+        const int off = __ldg(p.slot_map + t + i) & (sb - 1);
+        *reinterpret_cast<uint2*>(base + off * row) = encode8(load(i), inv);
+    }
+}
+
+// ------------------------------------------------------------------------------ gather
+struct Kv8GatherParams {
+    struct Side {
+        const uint8_t* codes;
+        const float* scale;
+        __nv_bfloat16* out;  // [total, Hkv, D]
+    };
+    Side k, v;
+    const int* block_table;   // [B, max_pages]
+    const int* cu_seqlens_k;  // [B + 1]
+    int B, total, Hkv, D, num_pages, page_shift, sb_shift, max_pages;
+};
+
+// kGatherRows packed rows of K or V (blockIdx.y) per CTA: their source rows are looked up
+// once, then every thread converts eight elements at a time.
+constexpr int kGatherRows = 16;
+__global__ void __launch_bounds__(256) kv8_gather(const Kv8GatherParams p) {
+    __shared__ int src[kGatherRows];  // row of the pool, -1: none
+    const int row0 = blockIdx.x * kGatherRows;
+    if (threadIdx.x < kGatherRows) {
+        const int t = row0 + threadIdx.x;
+        int s = -1;
+        if (t < p.total && t < __ldg(p.cu_seqlens_k + p.B)) {
+            const int b = owner_of(p.cu_seqlens_k, p.B, t);
+            const int pos = t - __ldg(p.cu_seqlens_k + b);
+            const int lp = pos >> p.page_shift;
+            int page = (pos >= 0 && lp < p.max_pages)
+                           ? __ldg(p.block_table + size_t(b) * p.max_pages + lp)
+                           : -1;
+            if (page < 0 || page >= p.num_pages) {
+                raise_device_error(kDevBadKvIndex);
+                page = 0;
+            }
+            s = (page << p.page_shift) + (pos & ((1 << p.page_shift) - 1));
+        }
+        src[threadIdx.x] = s;
+    }
+    __syncthreads();
+    const Kv8GatherParams::Side& io = blockIdx.y == 0 ? p.k : p.v;
+    const int chunks = p.Hkv * p.D / 8;  // of one row
+    for (int e = threadIdx.x; e < kGatherRows * chunks; e += blockDim.x) {
+        const int i = e / chunks, c = e - i * chunks;
+        const int s = src[i];
+        if (s < 0) continue;
+        const int h = c * 8 / p.D;
+        const float f = __ldg(io.scale + size_t(s >> p.sb_shift) * p.Hkv + h);
+        const uint2 o =
+            __ldg(reinterpret_cast<const uint2*>(io.codes + size_t(s) * chunks * 8) + c);
+        float y[4], z[4];
+        decode4(o.x, y);
+        decode4(o.y, z);
+        reinterpret_cast<uint4*>(io.out + size_t(row0 + i) * chunks * 8)[c] = make_uint4(
+            pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f),
+            pack_bf16x2(z[0] * f, z[1] * f), pack_bf16x2(z[2] * f, z[3] * f));
+    }
+}
+
+}  // namespace gqa

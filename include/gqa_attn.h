@@ -187,7 +187,8 @@ int gqa_attn_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, float scale, in
 /*
  * Read and clear the device error word on `stream` (synchronises that stream).
  * *host_code: 0 none, 1 a pipeline wait timed out, 2 a packed sequence is longer
- * than the Sq that was passed, 3 a KV-cache length or page index outside the cache.
+ * than the Sq that was passed, 3 a KV-cache length or page index outside the cache,
+ * 4 gqa_attn_kv_tables was short of free pages, of slots or of a block table's row.
  */
 int gqa_attn_get_device_error(int* host_code, cudaStream_t stream);
 
@@ -431,6 +432,104 @@ int gqa_attn_decode_fp8(const void* q, const void* k8, const void* v8, float k_s
                         float* lse, int B, int Hq, int Hkv, int D, int Sk, int num_pages,
                         int page_size, int max_pages, int max_seqlen_k, float scale, int window,
                         int num_splits, int pack_gqa, cudaStream_t stream);
+
+/*
+ * The 8-bit paged KV cache with a scale for each block of tokens and head.  One serving
+ * step: gqa_attn_kv_tables gives the new tokens their pages and slots, gqa_attn_kv8_append
+ * writes them, gqa_attn_kv8_decode attends to the cache (and gqa_attn_kv8_gather reads it
+ * back for a prefill); nothing in it waits for the host.
+ *   k8, v8 [num_pages, page_size, Hkv, D] e4m3 codes (as gqa_attn_decode_fp8's; the NaN
+ *     codes 0x7f and 0xff stand for NaN), D 64 or 128;
+ *   k_scale, v_scale fp32 [num_pages, page_size / scale_block, Hkv];
+ *   value = value(code) * scale of its block of scale_block tokens and head;
+ *   page_size and scale_block powers of two, 16 <= scale_block <= page_size, num_pages *
+ *     page_size < 2^31;
+ *   slot = page * page_size + position within the page.
+ *
+ * gqa_attn_kv_tables: block table rows, slot map and prefix sums of one step, from the
+ * requests' lengths, all on the device (int32 throughout).  For request b with
+ * cached_lens[b] tokens cached and new_lens[b] to come, ps = page_size, p0 =
+ * ceil(cached / ps) and p1 = ceil((cached + new) / ps):
+ *   block_table[b, p] for p0 <= p < p1 receives the next free pages: request b's are
+ *     free_pages[f], f counting up from *free_start (free_start NULL: 0) over the
+ *     requests in order; its other entries stay as they are, and the entry of a
+ *     partly filled page of cached tokens is read;
+ *   seqlens_k[b] = cached + new; cu_seqlens_q, cu_seqlens_k [B + 1] the prefix sums of
+ *     new_lens and of seqlens_k (at most 2^31 - 1);
+ *   slot_map[cu_seqlens_q[b] + i] = slot of position cached + i; -1 from
+ *     cu_seqlens_q[B] to max_tokens;
+ *   *free_end = *free_start + the pages taken: the next step's free_start (a buffer of
+ *     its own: GQA_ERR_SHAPE if it is free_start's).
+ * Device error 4: a negative length, one past max_pages * page_size (both are clamped),
+ * more tokens than max_tokens (the rest get no slot) or fewer free pages than needed
+ * (*free_end > n_free; the entries and slots without a page are -1).  B <= 16384.
+ */
+int gqa_attn_kv_tables(const int* cached_lens, const int* new_lens, const int* free_pages,
+                       const int* free_start, int* block_table, int* slot_map, int* seqlens_k,
+                       int* cu_seqlens_q, int* cu_seqlens_k, int* free_end, int B, int n_free,
+                       int max_pages, int page_size, int max_tokens, cudaStream_t stream);
+
+/*
+ * Writes T new tokens' keys and values into the cache.  k, v bf16 [T, Hkv, D], the heads
+ * of a token contiguous and tokens k_stride / v_stride elements apart (multiples of 8:
+ * a slice of a fused projection will do); slot_map int32 [T], -1 for rows to leave out.
+ * For each scale block that receives tokens, and each head of K and of V:
+ *   a = the largest |x| of its new tokens (infinity counts as the largest finite bf16, NaN
+ *     is passed over) and s_new the smallest power of two >= 2^-126 with a <= 448 s_new;
+ *   if position 0 of the block is among them the block starts anew, s = s_new;
+ *   otherwise s = max(s_new, the block's scale, rounded up to a power of two), and when
+ *     that changes the scale every other position's code becomes e4m3(code * old / s)
+ *     (a scale that is not finite and positive counts as none, and codes stay);
+ *   code = e4m3(x / s), rounded to nearest even, and the block's scale = s.
+ * All of one block's tokens must be neighbours in slot_map (their order is free) and the
+ * slots distinct, as gqa_attn_kv_tables makes them; otherwise the blocks concerned hold
+ * undefined codes and scales.  A slot outside the pool raises device error 3 and is left
+ * out.
+ */
+int gqa_attn_kv8_append(const void* k, const void* v, const int* slot_map, void* k8, void* v8,
+                        float* k_scale, float* v_scale, int T, int Hkv, int D,
+                        long long k_stride, long long v_stride, int num_pages, int page_size,
+                        int scale_block, cudaStream_t stream);
+
+/*
+ * The cache's values back as packed bf16 rows k, v [total, Hkv, D] (code * scale rounded to
+ * bf16, exact for the scales gqa_attn_kv8_append writes unless it leaves bf16's range):
+ * row cu_seqlens_k[b] + j is position j of sequence b, found through block_table [B,
+ * max_pages].  For a chunk's prefill with gqa_attn_fwd over cached tokens.  Rows from
+ * cu_seqlens_k[B] to total are left as they are; a table entry outside the pool raises
+ * device error 3 and page 0 is read in its place.
+ */
+int gqa_attn_kv8_gather(const void* k8, const void* v8, const float* k_scale,
+                        const float* v_scale, const int* block_table, const int* cu_seqlens_k,
+                        void* k, void* v, int B, int total, int Hkv, int D, int num_pages,
+                        int page_size, int max_pages, int scale_block, cudaStream_t stream);
+
+/*
+ * Attention of each sequence's newest positions over the cache: one (decode) or several
+ * (drafted tokens to verify).  Sequence b has L = seqlens_k[b] keys, its n_b queries
+ * among them the last n_b positions; query i sees keys j with
+ *   j <= L - n_b + i, and j > L - n_b + i - window when window > 0;
+ *   out = softmax(scale * q k^T) v and lse as gqa_attn_decode_paged on the stored values;
+ *   a query that sees no key gets out = 0, lse = -inf.
+ *   cu_seqlens_q NULL: q, out bf16 [B, Sq, Hq, D], lse fp32 [B, Hq, Sq], n_b = Sq;
+ *   else packed: q, out [total_q, Hq, D], lse [Hq, total_q], n_b = cu_seqlens_q[b + 1] -
+ *     cu_seqlens_q[b] <= Sq; rows from cu_seqlens_q[B] to total_q are left as they are
+ *     (a range that does not fit raises device error 2 and is left out).
+ *   block_table [B, max_pages], seqlens_k [B]: as gqa_attn_decode_paged; only entries of
+ *     pages that hold a visible key are read.
+ * Scales: any finite positive fp32.  What lies in the pool outside the visible keys is
+ * never used, whatever its codes.  workspace: gqa_attn_kv8_decode_workspace_bytes(B, Sq, Hq,
+ * Hkv, D) bytes, 16-byte aligned, private to the call until it has run: a parameter and
+ * not the registered workspace, so that calls on several streams and in several captured
+ * graphs do not share one.
+ */
+size_t gqa_attn_kv8_decode_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D);
+int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const float* k_scale,
+                        const float* v_scale, const int* block_table, const int* seqlens_k,
+                        const int* cu_seqlens_q, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, int B, int Sq, int total_q, int Hq, int Hkv,
+                        int D, int num_pages, int page_size, int max_pages, int scale_block,
+                        float scale, int window, cudaStream_t stream);
 
 /*
  * Diagnostic: exercises the kernels' bounded-wait path.  Launches one warp that
