@@ -1,5 +1,37 @@
 // Attention of the newest positions of each sequence over the 8-bit paged cache with block
-// scales (kv8_cache.cuh).
+// scales (kv8_cache.cuh): one position (decode) or a few (drafted tokens).
+//
+// Bound: HBM.  Every visible key and value is read once, at one byte an element, for about
+// four operations a byte; the kernel's task is to keep the copies streaming.
+//
+// Both products run on the 8-bit codes as they lie in the cache, with no conversion: the
+// 5th-generation MMA takes e4m3 operands from shared memory, and its M side (128 wide)
+// holds what is long,
+//   S^T [128 keys, rows]  = K tile [128 keys, 128 bytes]   x Q^T,
+//   O^T [128 dims, rows]  = V tile^T [128 dims, 128 keys]  x P^T,
+// so that one thread owns one key in the softmax and one dimension in the output.  The bf16
+// (q) and fp32 (p) sides are each split into two e4m3 terms, x = hi + lo / 2^n: e4m3 keeps
+// four significant bits, so hi holds the upper four of bf16's eight, and the remainder, at
+// most half a unit of hi's last place, fits the other term: q is exact (down to 2^-21 of
+// its row's largest element) and p is rounded at 2^-8 of itself, as it would be in bf16.
+// The terms are further columns of the same MMA, whose N side has room.
+//
+// Scales: a key's K scale multiplies its logit.  Its V scale is folded into its weight,
+// relative to the largest V scale of the tile (vref), which comes back when the tile's
+// O^T is added to the fp32 sum held in registers.  With z the logit in log2 units and
+// d = log2(vs / vref) <= 0, a tile's reference is max_j (z_j + max(d_j, -60)) and the
+// running reference m its maximum over the tiles: weights 2^(z - m) vs / vref stay at or
+// below 1 where they are rounded, and the normaliser's terms 2^(z - m) at or below 2^60,
+// however unlike the scales of neighbouring blocks are.
+//
+// Heads of 64 dimensions go in pairs: a 128-byte row holds two KV heads, each query row is
+// padded with zeros in the other's half, and each half of O^T is read by its own head's
+// rows (the MMA's idle half costs nothing here).
+//
+// Work: the (sequence, head group, row unit) items are laid end to end, in tiles of 128
+// keys, and every CTA of a fixed grid takes an equal range of them, whatever the lengths.
+// An item that ends up in several CTAs leaves one fp32 partial in each, joined by
+// kv8_combine, a programmatic dependent launch.
 #pragma once
 #include "kv8_cache.cuh"
 
@@ -9,98 +41,693 @@ struct Kv8DecodeParams {
     const __nv_bfloat16* q;   // [rows, Hq, D]
     __nv_bfloat16* out;       // like q
     float* lse;               // dense [B, Hq, Sq], packed [Hq, total_q]
-    const uint8_t* k8;
-    const uint8_t* v8;
     const float* k_scale;     // [num_pages * page_size / sb, Hkv]
     const float* v_scale;
     const int* block_table;   // [B, max_pages]
     const int* seqlens_k;     // [B]
     const int* cu_seqlens_q;  // [B + 1] or null: Sq queries each
+    float* part_o;            // [grid, 2, R, 128] fp32 partials of a CTA's cut items
+    float2* part_ml;          // [grid, 2, R] reference (log2 units) and sum
+    long long* meta;          // [items]: an item's first tile; [items]: all tiles
     int B, Sq, total_q, Hq, Hkv, G;
+    int groups, units;        // head groups (KV heads, or pairs of them); row units of each
+    int grid;                 // CTAs of kv8_decode
     int num_pages, page_shift, sb_shift, max_pages, window;
     float scale_log2;
 };
 
-// One CTA per (query head, query, sequence); each of its four warps takes every fourth
-// key, with an online softmax of its own, and the four are joined at the end.
-template <int D>
-__global__ void __launch_bounds__(128) kv8_decode_simple(const Kv8DecodeParams p) {
-    constexpr int PER = D / 32;
-    const int h = blockIdx.x, i = blockIdx.y, b = blockIdx.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int q0 = b * p.Sq, n = p.Sq;
+// ROWS query rows (query head x position, of both heads of a pair) per CTA and pass
+template <int ROWS>
+struct Kv8Cfg {
+    static constexpr int TILE = 128 * 128;              // bytes of K or V per stage
+    static constexpr int ST = 2;                        // stages of each
+    static constexpr int N = ROWS <= 8 ? 16 : 2 * ROWS;  // MMA columns: hi and lo of each row
+    static constexpr int OFF_K = 0;
+    static constexpr int OFF_V = ST * TILE;
+    static constexpr int OFF_Q = 2 * ST * TILE;
+    static constexpr int OFF_P = OFF_Q + N * 128;
+    static constexpr int OFF_SC = OFF_P + N * 128;      // [ST][2 halves][8 groups] float4
+    static constexpr int OFF_VREF = OFF_SC + ST * 256;  // [ST][2]
+    static constexpr int OFF_RED = OFF_VREF + ST * 8;   // [4 warps][ROWS]
+    static constexpr int OFF_QF = OFF_RED + 16 * ROWS;  // [ROWS]
+    static constexpr int OFF_BAR = OFF_QF + 4 * ROWS;
+    static constexpr int N_BAR = 5 * ST + 2;
+    static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
+    static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
+    static constexpr int TMEM_COLS = 2 * N;             // S^T and O^T
+    static constexpr int THREADS = 160;
+    static constexpr int CTAS_PER_SM = ROWS <= 16 ? 3 : 2;
+};
+
+struct Kv8Seq {
+    int q0, n, len;  // first query row, queries, keys
+};
+__device__ __forceinline__ Kv8Seq kv8_seq(const Kv8DecodeParams& p, int b) {
+    Kv8Seq s;
+    s.q0 = b * p.Sq;
+    s.n = p.Sq;
     if (p.cu_seqlens_q) {
-        q0 = __ldg(p.cu_seqlens_q + b);
-        n = __ldg(p.cu_seqlens_q + b + 1) - q0;
-        if (n < 0 || n > p.Sq || q0 < 0 || q0 > p.total_q - n) {
+        s.q0 = __ldg(p.cu_seqlens_q + b);
+        s.n = __ldg(p.cu_seqlens_q + b + 1) - s.q0;
+        if (s.n < 0 || s.n > p.Sq || s.q0 < 0 || s.q0 > p.total_q - s.n) {
             raise_device_error(kDevBadTile);
-            return;
+            s.n = 0;
         }
     }
-    if (i >= n) return;
     const int cap = p.max_pages << p.page_shift;
-    int len = __ldg(p.seqlens_k + b);
-    if (len < 0 || len > cap) {
+    s.len = __ldg(p.seqlens_k + b);
+    if (s.len < 0 || s.len > cap) {
         raise_device_error(kDevBadKvIndex);
-        len = min(max(len, 0), cap);
+        s.len = min(max(s.len, 0), cap);
     }
-    const int end = max(len - n + i + 1, 0);
-    const int start = p.window > 0 ? max(end - p.window, 0) : 0;
-    const int kvh = h / p.G;
-    const size_t row = size_t(q0 + i) * p.Hq + h;
-    float q[PER], o[PER];
-    for (int e = 0; e < PER; ++e) {
-        q[e] = __bfloat162float(p.q[row * D + lane * PER + e]);
-        o[e] = 0.f;
+    return s;
+}
+
+// Keys [lo, hi) that some row of unit u sees (SUB positions x heads of one KV head each)
+struct Kv8Keys {
+    int lo, hi;
+    __device__ __forceinline__ int first() const { return lo >> 7; }
+    __device__ __forceinline__ int tiles() const { return hi > lo ? ((hi + 127) >> 7) - (lo >> 7) : 0; }
+};
+template <int SUB>
+__device__ __forceinline__ Kv8Keys kv8_keys(const Kv8DecodeParams& p, const Kv8Seq& s, int u) {
+    const int i0 = u * SUB / p.G;
+    const int i1 = min((u * SUB + SUB - 1) / p.G, s.n - 1);
+    Kv8Keys k = {0, 0};
+    if (i0 < s.n) {
+        k.hi = max(s.len - s.n + i1 + 1, 0);
+        if (p.window > 0) k.lo = max(s.len - s.n + i0 + 1 - p.window, 0);
     }
-    float m = -INFINITY, l = 0.f;
-    for (int j = start + warp; j < end; j += 4) {
-        int page = __ldg(p.block_table + size_t(b) * p.max_pages + (j >> p.page_shift));
-        if (page < 0 || page >= p.num_pages) {
-            raise_device_error(kDevBadKvIndex);
-            page = 0;
+    return k;
+}
+
+// A CTA's walk over its range of tiles: segments of consecutive items.
+template <int SUB>
+struct Kv8Walk {
+    int b, hg, u;        // the item
+    int off;             // its tiles already passed
+    long long left;      // tiles of this CTA still to come
+    Kv8Seq seq;
+    Kv8Keys keys;
+    int n;               // its tiles
+    __device__ __forceinline__ void load(const Kv8DecodeParams& p) {
+        keys = kv8_keys<SUB>(p, seq, u);
+        n = keys.tiles();
+    }
+    __device__ __forceinline__ void start(const Kv8DecodeParams& p, int b_, int hg_, int u_,
+                                          int off_, long long left_) {
+        b = b_, hg = hg_, u = u_, off = off_, left = left_;
+        if (left > 0) {
+            seq = kv8_seq(p, b);
+            load(p);
         }
-        const int s = (page << p.page_shift) + (j & ((1 << p.page_shift) - 1));
-        const size_t at = (size_t(s) * p.Hkv + kvh) * D + lane * PER;
-        const size_t sc = size_t(s >> p.sb_shift) * p.Hkv + kvh;
-        float acc = 0.f, x[4];
-        uint32_t w = 0;
-        for (int e = 0; e < PER; ++e) w |= uint32_t(p.k8[at + e]) << (8 * e);
-        decode4(w, x);
-        for (int e = 0; e < PER; ++e) acc += q[e] * x[e];
-        for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
-        const float z = acc * p.k_scale[sc] * p.scale_log2;
-        const float m1 = fmaxf(m, z);
-        const float alpha = exp2f(m - m1), u = exp2f(z - m1);
-        w = 0;
-        for (int e = 0; e < PER; ++e) w |= uint32_t(p.v8[at + e]) << (8 * e);
-        decode4(w, x);
-        const float f = u * p.v_scale[sc];
-        for (int e = 0; e < PER; ++e) o[e] = o[e] * alpha + f * x[e];
-        l = l * alpha + u;
-        m = m1;
     }
-    __shared__ float so[4][D], sm[4], sl[4];
-    for (int e = 0; e < PER; ++e) so[warp][lane * PER + e] = o[e];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
+    __device__ __forceinline__ int segment() const {
+        return int(min((long long)(n - off), left));
     }
+    __device__ __forceinline__ void next(const Kv8DecodeParams& p) {
+        left -= segment();
+        off = 0;
+        if (left <= 0) return;
+        do {
+            if (++u == p.units) {
+                u = 0;
+                if (++hg == p.groups) {
+                    hg = 0;
+                    seq = kv8_seq(p, ++b);
+                }
+            }
+            load(p);
+        } while (n == 0);
+    }
+};
+
+// First tile of CTA `cta` of `ctas` (those with work: a tile each at least)
+__device__ __forceinline__ int kv8_ctas(long long tiles, int grid) {
+    return int(min(tiles, (long long)grid));
+}
+__device__ __forceinline__ long long kv8_range_start(long long tiles, int cta, int ctas) {
+    return tiles * cta / ctas;
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+// Rows [r0, r0 + C) of an accumulator whose column r is row r's hi term and column ROWS + r
+// its lo term: f = hi + lo * w.
+template <int ROWS, int C>
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, int r0, float w, float (&f)[C]) {
+    static_assert((ROWS == 4 && C == 4) || C == 8, "");
+    uint32_t a[8], b[8];
+    tmem_ld8(taddr + r0, a);
+    if constexpr (C == 8) tmem_ld8(taddr + ROWS + r0, b);
+    tmem_ld_wait();
+    reg_fence(a);
+    if constexpr (C == 8) reg_fence(b);
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        f[i] = fmaf(__uint_as_float(C == 8 ? b[i] : a[4 + i]), w, __uint_as_float(a[i]));
+}
+
+// x0, x1 as two e4m3 terms each: hi (bytes: x0, x1) and lo, x = hi + lo / shift
+__device__ __forceinline__ void split_e4m3x2(float x0, float x1, float shift, uint16_t& hi,
+                                             uint16_t& lo) {
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x1), "f"(x0));
+    uint32_t back;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
+    add_f16x2_to_f32(back ^ 0x80008000u, x0, x1);
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+        : "=h"(lo)
+        : "f"(x1 * shift), "f"(x0 * shift));
+}
+__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ float warp_max(float x) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool consumers_any(bool x) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(int(x))
+        : "memory");
+    return r != 0;
+}
+
+// Where row `r` of unit u belongs: position i of its sequence and query head h
+template <int ROWS, bool PAIR>
+__device__ __forceinline__ bool kv8_row(const Kv8DecodeParams& p, const Kv8Seq& s, int hg, int u,
+                                        int r, int& i, int& h) {
+    constexpr int SUB = PAIR ? ROWS / 2 : ROWS;
+    const int half = PAIR ? r / SUB : 0;
+    const int sub = u * SUB + (r - half * SUB);
+    const int kvh = PAIR ? 2 * hg + half : hg;
+    i = sub / p.G;
+    h = kvh * p.G + (sub - i * p.G);
+    return i < s.n && kvh < p.Hkv;
+}
+
+template <int ROWS, bool PAIR>
+__global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_SM)
+    kv8_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+               const Kv8DecodeParams p) {
+    using C = Kv8Cfg<ROWS>;
+    constexpr int SUB = PAIR ? ROWS / 2 : ROWS;
+    constexpr int CH = ROWS < 8 ? ROWS : 8;  // rows per accumulator load
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full_k = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* empty_k = full_k + C::ST;
+    uint64_t* full_v = empty_k + C::ST;
+    uint64_t* empty_v = full_v + C::ST;
+    uint64_t* full_s = empty_v + C::ST;
+    uint64_t* s_done = full_s + C::ST;
+    uint64_t* o_done = s_done + 1;
+    int* misc = reinterpret_cast<int*>(smem + C::OFF_MISC);
+    volatile int* abort_flag = misc;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
+    volatile int* first_item = misc + 2;                                   // b, hg, u, off
+    volatile long long* range = reinterpret_cast<volatile long long*>(misc + 6);  // left, first tile
+    long long* scan = reinterpret_cast<long long*>(smem + C::OFF_P);       // before P is used
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    griddep_launch_dependents();
+    if (tid == 0) {
+        for (int s = 0; s < C::ST; ++s) {
+            mbar_init(full_k + s, 1);
+            mbar_init(empty_k + s, 1);
+            mbar_init(full_v + s, 1);
+            mbar_init(empty_v + s, 1);
+            mbar_init(full_s + s, 1);
+        }
+        mbar_init(s_done, 1);
+        mbar_init(o_done, 1);
+        *abort_flag = 0;
+        range[0] = 0;
+        fence_mbar_init();
+    }
+    if (warp == 4) tmem_alloc(tmem_slot, C::TMEM_COLS);
+
+    // Every CTA adds up all tiles and finds the item its own range starts in.
+    {
+        const int per = (p.B + C::THREADS - 1) / C::THREADS;
+        const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+        auto tiles_of = [&](int b) {  // of one head group
+            const Kv8Seq s = kv8_seq(p, b);
+            long long t = 0;
+            for (int u = 0; u < p.units; ++u) t += kv8_keys<SUB>(p, s, u).tiles();
+            return t;
+        };
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += tiles_of(b) * p.groups;
+        long long inc = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += o;
+        }
+        if (lane == 31) scan[warp] = inc;
+        __syncthreads();
+        long long before = inc - mine, all = 0;
+        for (int w = 0; w < C::THREADS / 32; ++w) {
+            if (w < warp) before += scan[w];
+            all += scan[w];
+        }
+        const int ctas = kv8_ctas(all, p.grid);
+        const bool works = int(blockIdx.x) < ctas;
+        const long long lo = works ? kv8_range_start(all, blockIdx.x, ctas) : 0;
+        const long long hi = works ? kv8_range_start(all, blockIdx.x + 1, ctas) : 0;
+        if (blockIdx.x == 0 && tid == 0) p.meta[(long long)p.B * p.groups * p.units] = all;
+        if (lo < hi && lo >= before && lo < before + mine) {
+            long long at = lo - before;
+            int b = b0;
+            long long t = tiles_of(b);
+            while (at >= t * p.groups) {
+                at -= t * p.groups;
+                t = tiles_of(++b);
+            }
+            const int hg = int(at / t);
+            at -= hg * t;
+            const Kv8Seq s = kv8_seq(p, b);
+            int u = 0, n = kv8_keys<SUB>(p, s, 0).tiles();
+            while (at >= n) {
+                at -= n;
+                n = kv8_keys<SUB>(p, s, ++u).tiles();
+            }
+            first_item[0] = b;
+            first_item[1] = hg;
+            first_item[2] = u;
+            first_item[3] = int(at);
+            range[0] = hi - lo;
+            range[1] = lo;
+        }
+    }
+    tc_fence_before();
     __syncthreads();
-    const float M = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-    float L = 0.f, acc = 0.f;
-    for (int w = 0; w < 4; ++w) {
-        const float f = M == -INFINITY ? 0.f : exp2f(sm[w] - M);
-        L += f * sl[w];
-        if (threadIdx.x < D) acc += f * so[w][threadIdx.x];
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Kv8Walk<SUB> walk;
+    walk.start(p, first_item[0], first_item[1], first_item[2], first_item[3], range[0]);
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ producer
+        // A tile is one copy per page it touches (128 rows at most), one lane each, and the
+        // scales of its eight groups of 16 keys (a scale block is 16 keys or more): lane
+        // 8 * half + group fetches those of its group.  Their loads are under way while the
+        // lanes wait for free stages.
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_v);
+        }
+        const int box = min(1 << p.page_shift, 128), boxes = 128 / box;
+        const int half = (lane >> 3) & 1, grp = lane & 7;
+        int c = 0, copies[2] = {0, 0};  // tiles; copies of K and of V issued
+        bool ok = true;
+        for (; walk.left > 0 && ok; walk.next(p)) {
+            const int* row = p.block_table + size_t(walk.b) * p.max_pages;
+            const int x = walk.hg * 128;
+            const int kvh = PAIR ? 2 * walk.hg + half : walk.hg;
+            const bool here = lane < (PAIR ? 16 : 8) && kvh < p.Hkv;
+            const int t1 = walk.keys.first() + walk.off + walk.segment();
+            for (int t = walk.keys.first() + walk.off; t < t1 && ok; ++t, ++c) {
+                auto slot_of = [&](int key, int at) {  // row `at` of the page that holds `key`
+                    int page = __ldg(row + (key >> p.page_shift));
+                    if (page < 0 || page >= p.num_pages) {
+                        raise_device_error(kDevBadKvIndex);
+                        page = 0;
+                    }
+                    return (page << p.page_shift) + (at & ((1 << p.page_shift) - 1));
+                };
+                int z = 0;
+                if (lane < boxes) {
+                    // rows without a visible key are read from a page that has one: their
+                    // own table entry may name no page
+                    const int a = t * 128 + lane * box;
+                    const bool seen = a < walk.keys.hi && a + box > walk.keys.lo;
+                    z = slot_of(seen ? a : max(walk.keys.lo, t * 128), a);
+                }
+                const int a = t * 128 + grp * 16;
+                float ks = 0.f, vs = 0.f;
+                if (here && a < walk.keys.hi && a + 16 > walk.keys.lo) {
+                    const size_t at = size_t(slot_of(a, a) >> p.sb_shift) * p.Hkv + kvh;
+                    ks = __ldg(p.k_scale + at);
+                    vs = __ldg(p.v_scale + at);
+                }
+                const int s = c % C::ST;
+                const uint32_t ph = ((c / C::ST) & 1) ^ 1;
+                ok = mbar_wait_warp(empty_k + s, ph, abort_flag);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(full_k + s, C::TILE);
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_2d(smem + C::OFF_K + s * C::TILE + lane * box * 128, &tm_k,
+                                full_k + s, x, z);
+                ++copies[0];
+                ok = mbar_wait_warp(empty_v + s, ph, abort_flag);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(full_v + s, C::TILE);
+                __syncwarp();
+                if (lane < boxes)
+                    tma_load_2d(smem + C::OFF_V + s * C::TILE + lane * box * 128, &tm_v,
+                                full_v + s, x, z);
+                ++copies[1];
+                // V's stage being free, so is the stage of scales: all four consumer warps
+                // have read them before that tile's P V was issued
+                float vref = vs;
+#pragma unroll
+                for (int off = 4; off > 0; off >>= 1)
+                    vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, off));
+                const float rel = vref > 0.f ? vs / vref : 0.f;
+                if (lane < 16)
+                    reinterpret_cast<float4*>(smem + C::OFF_SC)[s * 16 + lane] =
+                        make_float4(ks, fmaxf(__log2f(rel), -60.f), rel * 128.f, 0.f);
+                if (lane < 16 && grp == 0)
+                    reinterpret_cast<float*>(smem + C::OFF_VREF)[s * 2 + half] =
+                        vref * 0.0078125f;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full_s + s);
+            }
+        }
+        // every issued copy lands before the CTA may release the memory
+        if (lane == 0) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv)
+                for (int s = 0; s < C::ST; ++s) {
+                    const int n = copies[kv] / C::ST + (s < copies[kv] % C::ST ? 1 : 0);
+                    const uint64_t t0 = globaltimer_ns();
+                    while (n > 0 && !mbar_try_wait((kv ? full_v : full_k) + s, (n - 1) & 1))
+                        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                            raise_device_error(kDevWaitTimeout);
+                            break;
+                        }
+                }
+        }
+    } else {
+        // ------------------------------------------------------------ consumers
+        const uint32_t idesc_s = idesc_e4m3_f32(128, C::N, 0, 0);
+        const uint32_t idesc_o = idesc_e4m3_f32(128, C::N, 1, 0);
+        const uint64_t dk = sw128_desc(smem_u32(smem + C::OFF_K), 16, 1024);
+        const uint64_t dv = sw128_desc(smem_u32(smem + C::OFF_V), C::TILE, 1024);
+        const uint64_t dq = sw128_desc(smem_u32(smem + C::OFF_Q), 16, 1024);
+        const uint64_t dp = sw128_desc(smem_u32(smem + C::OFF_P), 16, 1024);
+        const uint32_t lane_base = uint32_t(warp * 32) << 16;  // this warp's TMEM lanes
+        const uint32_t t_s = tmem + lane_base, t_o = t_s + C::N;
+        const uint32_t sq = smem_u32(smem + C::OFF_Q);
+        // this thread's key column of P (row r: + r * 128, chunk xor r & 7)
+        const uint32_t sp = smem_u32(smem + C::OFF_P) + (tid & 15);
+        float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
+        float* qf = reinterpret_cast<float*>(smem + C::OFF_QF);
+        const int my_half = PAIR ? tid >> 6 : 0;  // of this thread's dimension
+        int c = 0;
+        bool aborted = false, first_segment = true;
+        for (; walk.left > 0; walk.next(p), first_segment = false) {
+            const int segment = walk.segment();
+            const bool whole = walk.off == 0 && segment == walk.n;
+            // --- q rows of this item as two e4m3 terms; the MMAs that read the last
+            // item's rows have completed
+            for (int r = warp; r < ROWS; r += 4) {
+                int i, h;
+                const bool valid = kv8_row<ROWS, PAIR>(p, walk.seq, walk.hg, walk.u, r, i, h);
+                constexpr int D = PAIR ? 64 : 128;
+                const int d0 = PAIR ? (lane * 4) & 63 : lane * 4;
+                const bool in = valid && (!PAIR || (lane >> 4) == r / SUB);
+                uint2 w = make_uint2(0u, 0u);
+                if (in)
+                    w = __ldg(reinterpret_cast<const uint2*>(
+                        p.q + (size_t(walk.seq.q0 + i) * p.Hq + h) * D + d0));
+                const uint32_t big = max(max((w.x << 16) & 0x7fffffffu, w.x & 0x7fff0000u),
+                                         max((w.y << 16) & 0x7fffffffu, w.y & 0x7fff0000u));
+                const uint32_t amax = __reduce_max_sync(0xffffffffu, big);
+                // power-of-two factor that brings the row's largest |q| to [128, 256)
+                const int e = max(int(amax >> 23), 8);
+                const float up = __uint_as_float(uint32_t(261 - e) << 23);
+                uint16_t hi[2], lo[2];
+                split_e4m3x2(bf16_lo(w.x) * up, bf16_hi(w.x) * up, 16.f, hi[0], lo[0]);
+                split_e4m3x2(bf16_lo(w.y) * up, bf16_hi(w.y) * up, 16.f, hi[1], lo[1]);
+                const uint32_t at = (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+                const uint32_t row_hi = sq + r * 128 + at;
+                const uint32_t row_lo = sq + (ROWS + r) * 128 +
+                                        (((lane >> 2) ^ ((ROWS + r) & 7)) << 4) + (lane & 3) * 4;
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(row_hi),
+                             "r"(uint32_t(hi[0]) | uint32_t(hi[1]) << 16)
+                             : "memory");
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(row_lo),
+                             "r"(uint32_t(lo[0]) | uint32_t(lo[1]) << 16)
+                             : "memory");
+                // a row with an infinity or a NaN has no factor: its logits are NaN
+                if (lane == 0)
+                    qf[r] = amax >= 0x7f800000u ? NAN
+                                                : __uint_as_float(uint32_t(e - 7) << 23) *
+                                                      p.scale_log2;
+            }
+            fence_proxy_async();
+            consumers_sync();
+
+            float m[ROWS], l[ROWS], o[ROWS];
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) m[r] = -INFINITY, l[r] = 0.f, o[r] = 0.f;
+            // keys that every row sees, in tiles between which no mask is needed
+            const int t0 = walk.keys.first() + walk.off;
+            const int last = walk.seq.len - walk.seq.n;  // position of query 0
+            const int i_lo = walk.u * SUB / p.G;
+            const int i_hi = min((walk.u * SUB + SUB - 1) / p.G, walk.seq.n - 1);
+            const int all_hi = last + i_lo + 1;
+            const int all_lo = p.window > 0 ? max(last + i_hi + 1 - p.window, 0) : 0;
+            for (int t = t0; t < t0 + segment && !aborted; ++t, ++c) {
+                const int s = c % C::ST;
+                const uint32_t ph = (c / C::ST) & 1;
+                bool ok = true;
+                if (tid == 0) {
+                    ok = mbar_wait(full_k + s, ph, abort_flag);
+                    if (ok) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_ss_f8(tmem, dk + ((s * C::TILE + kk * 32) >> 4),
+                                       dq + ((kk * 32) >> 4), idesc_s, kk > 0);
+                        umma_commit(empty_k + s);
+                        umma_commit(s_done);
+                    }
+                }
+                __syncwarp();
+                const int key = t * 128 + tid;
+                ok &= mbar_wait_warp(full_s + s, ph, abort_flag);
+                float4 sc[2];
+                sc[0] = reinterpret_cast<float4*>(smem + C::OFF_SC)[s * 16 + (tid >> 4)];
+                if constexpr (PAIR)
+                    sc[1] = reinterpret_cast<float4*>(smem + C::OFF_SC)[s * 16 + 8 + (tid >> 4)];
+                const float vref =
+                    reinterpret_cast<float*>(smem + C::OFF_VREF)[s * 2 + my_half];
+                ok &= mbar_wait_warp(s_done, c & 1, abort_flag);
+                tc_fence_after();
+                const bool edge = t * 128 < all_lo || t * 128 + 128 > all_hi;
+                float z[ROWS];
+                float top = -INFINITY;  // lane r: the warp's largest z + d of row r
+#pragma unroll
+                for (int r0 = 0; r0 < ROWS; r0 += CH) {
+                    float f[CH];
+                    tmem_ld_rows<ROWS, CH>(t_s, r0, 0.0625f, f);
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) {
+                        const int r = r0 + j;
+                        const float4& k = sc[PAIR ? r / SUB : 0];
+                        z[r] = f[j] * (k.x * qf[r]);
+                        if (edge) {
+                            const int i = (walk.u * SUB + r % SUB) / p.G;
+                            const int hi = min(last + i + 1, walk.keys.hi);
+                            if (key >= hi || (p.window > 0 && key < last + i + 1 - p.window))
+                                z[r] = -INFINITY;
+                        }
+                        const float mx = warp_max(z[r] + k.y);
+                        if (lane == r) top = mx;
+                    }
+                }
+                if (lane < ROWS) red[warp * ROWS + lane] = top;
+                consumers_sync();
+#pragma unroll
+                for (int r = 0; r < ROWS; r += 2) {
+                    float w[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int a = r + j;
+                        const float mt = fmaxf(fmaxf(red[a], red[ROWS + a]),
+                                               fmaxf(red[2 * ROWS + a], red[3 * ROWS + a]));
+                        const float m1 = fmaxf(m[a], mt);
+                        const float mu = m1 == -INFINITY ? 0.f : m1;
+                        const float alpha = ex2_approx(m[a] - mu);
+                        const float u = ex2_approx(z[a] - mu);
+                        m[a] = m1;
+                        l[a] = fmaf(l[a], alpha, u);
+                        o[a] *= alpha;
+                        w[j] = u * sc[PAIR ? a / SUB : 0].z;
+                    }
+                    uint16_t hi, lo;
+                    split_e4m3x2(w[0], w[1], 32.f, hi, lo);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int a = r + j, b = ROWS + r + j;
+                        st_shared_u8(sp + a * 128 + (((tid >> 4) ^ (a & 7)) << 4), hi >> (8 * j));
+                        st_shared_u8(sp + b * 128 + (((tid >> 4) ^ (b & 7)) << 4), lo >> (8 * j));
+                    }
+                }
+                // V rows that no query sees may hold any code: a weight of 0 times NaN
+                // would still reach O
+                if (t * 128 < walk.keys.lo || t * 128 + 128 > walk.keys.hi) {
+                    ok &= mbar_wait_warp(full_v + s, ph, abort_flag);
+                    if (key < walk.keys.lo || key >= walk.keys.hi) {
+                        const uint32_t v = smem_u32(smem + C::OFF_V + s * C::TILE) + tid * 128;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) st_shared_v4(v + j * 16, 0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_proxy_async();
+                tc_fence_before();
+                aborted = consumers_any(!ok);
+                if (tid == 0 && !aborted) {
+                    ok = mbar_wait(full_v + s, ph, abort_flag);
+                    if (ok) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_ss_f8(tmem + C::N, dv + ((s * C::TILE + kk * 32 * 128) >> 4),
+                                       dp + ((kk * 32) >> 4), idesc_o, kk > 0);
+                        umma_commit(empty_v + s);
+                        umma_commit(o_done);
+                    }
+                }
+                __syncwarp();
+                // (a wait that runs out here shows in the next tile's waits, or below)
+                mbar_wait_warp(o_done, c & 1, abort_flag);
+                tc_fence_after();
+#pragma unroll
+                for (int r0 = 0; r0 < ROWS; r0 += CH) {
+                    float f[CH];
+                    tmem_ld_rows<ROWS, CH>(t_o, r0, 0.03125f, f);
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) o[r0 + j] = fmaf(f[j], vref, o[r0 + j]);
+                }
+                tc_fence_before();
+            }
+            // --- end of the segment: sums over the keys, then the rows' results
+            aborted = consumers_any(aborted || *abort_flag != 0);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1)
+                    l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
+                if (lane == 0) red[warp * ROWS + r] = l[r];
+            }
+            consumers_sync();
+            const long long item = ((long long)walk.b * p.groups + walk.hg) * p.units + walk.u;
+            const size_t part = size_t(blockIdx.x) * 2 + (first_segment ? 0 : 1);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                float sum = (red[r] + red[ROWS + r]) + (red[2 * ROWS + r] + red[3 * ROWS + r]);
+                if (aborted) {
+                    // a wait gave up (device error word set): an empty result, so that no
+                    // stale memory is picked up
+                    sum = 0.f, m[r] = -INFINITY, o[r] = 0.f;
+                }
+                if (!whole) {
+                    p.part_o[(part * ROWS + r) * 128 + tid] = o[r];
+                    if (tid == 0) p.part_ml[part * ROWS + r] = make_float2(m[r], sum);
+                    continue;
+                }
+                int i, h;
+                if (!kv8_row<ROWS, PAIR>(p, walk.seq, walk.hg, walk.u, r, i, h)) continue;
+                const size_t q_row = size_t(walk.seq.q0 + i) * p.Hq + h;
+                const float v = sum == 0.f ? 0.f : o[r] / sum;
+                if constexpr (PAIR) {
+                    if (my_half == r / SUB) p.out[q_row * 64 + (tid & 63)] = __float2bfloat16_rn(v);
+                } else {
+                    p.out[q_row * 128 + tid] = __float2bfloat16_rn(v);
+                }
+                if (tid == 0)
+                    p.lse[p.cu_seqlens_q ? size_t(h) * p.total_q + walk.seq.q0 + i
+                                         : (size_t(walk.b) * p.Hq + h) * p.Sq + i] =
+                        sum == 0.f ? -INFINITY : (m[r] + __log2f(sum)) * 0.69314718055994531f;
+            }
+            if (tid == 0 && walk.off == 0) p.meta[item] = range[1] + (range[0] - walk.left);
+            consumers_sync();  // red is free again
+        }
     }
-    if (threadIdx.x < D)
-        p.out[row * D + threadIdx.x] = __float2bfloat16_rn(L > 0.f ? acc / L : 0.f);
-    if (threadIdx.x == 0) {
-        const size_t at = p.cu_seqlens_q ? size_t(h) * p.total_q + q0 + i
-                                         : (size_t(b) * p.Hq + h) * p.Sq + i;
-        p.lse[at] = L > 0.f ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_relinquish();
+        tmem_dealloc(tmem, C::TMEM_COLS);
     }
+}
+
+// One CTA per (row, item): joins the partials of an item that several CTAs shared, and
+// writes the rows that no key reached.  With reference M = max_s m_s (log2 units):
+// sum = sum_s 2^(m_s - M) sum_s, O = sum_s 2^(m_s - M) O_s / sum, L = ln 2 (M + log2 sum).
+template <int ROWS, bool PAIR>
+__global__ void __launch_bounds__(128) kv8_combine(const Kv8DecodeParams p) {
+    constexpr int SUB = PAIR ? ROWS / 2 : ROWS;
+    const int r = blockIdx.x, tid = threadIdx.x;
+    const long long item = blockIdx.y + (long long)blockIdx.z * 65535;
+    const long long items = (long long)p.B * p.groups * p.units;
+    if (item >= items) return;
+    const int u = int(item % p.units);
+    const int hg = int(item / p.units % p.groups);
+    const int b = int(item / p.units / p.groups);
+    const Kv8Seq seq = kv8_seq(p, b);
+    int i, h;
+    if (!kv8_row<ROWS, PAIR>(p, seq, hg, u, r, i, h)) return;
+    const int n = kv8_keys<SUB>(p, seq, u).tiles();
+    const int half = PAIR ? r / SUB : 0;
+    griddep_wait();
+    float M = -INFINITY, sum = 0.f, acc = 0.f;
+    if (n > 0) {
+        const long long all = p.meta[items], first = p.meta[item];
+        const int ctas = kv8_ctas(all, p.grid);
+        const int c0 = int(((first + 1) * ctas - 1) / all);
+        const int c1 = int(((first + n) * ctas - 1) / all);
+        if (c0 == c1) return;  // one CTA has written it
+        // the first CTA's share is its second partial unless its range starts there
+        const bool cut = kv8_range_start(all, c0, ctas) != first;
+        auto part = [&](int c) { return size_t(c) * 2 + (c == c0 && cut ? 1 : 0); };
+        for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.part_ml[part(c) * ROWS + r].x);
+        for (int c = c0; c <= c1; ++c) {
+            const float2 ml = p.part_ml[part(c) * ROWS + r];
+            const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+            sum += f * ml.y;
+            acc += f * p.part_o[(part(c) * ROWS + r) * 128 + tid];
+        }
+    }
+    const size_t q_row = size_t(seq.q0 + i) * p.Hq + h;
+    const float v = sum == 0.f ? 0.f : acc / sum;
+    if constexpr (PAIR) {
+        if (tid >> 6 == half) p.out[q_row * 64 + (tid & 63)] = __float2bfloat16_rn(v);
+    } else {
+        p.out[q_row * 128 + tid] = __float2bfloat16_rn(v);
+    }
+    if (tid == 0)
+        p.lse[p.cu_seqlens_q ? size_t(h) * p.total_q + seq.q0 + i
+                             : (size_t(b) * p.Hq + h) * p.Sq + i] =
+            sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace gqa

@@ -2,6 +2,8 @@
 // (gqa_attn_kv_tables, gqa_attn_kv8_append, gqa_attn_kv8_gather, gqa_attn_kv8_decode).
 // Uses the argument checks and the device table of gqa_attn.cu.
 #pragma once
+#include <type_traits>
+
 #include "kv8_decode.cuh"
 
 namespace {
@@ -17,6 +19,45 @@ int check_pool(int num_pages, int page_size, int scale_block, int Hkv, int D) {
     if ((long long)num_pages * page_size > INT32_MAX || (long long)Hkv * D > (1 << 24))
         return GQA_ERR_SHAPE;
     return GQA_OK;
+}
+
+// The cache as rows of Hkv * D bytes, copied in boxes of 128 bytes (one head of 128
+// dimensions or two of 64) by box_rows, 128-byte swizzle.
+bool make_map_kv8(CUtensorMap* m, const void* base, long long rows, int width, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {cuuint64_t(width), cuuint64_t(rows)};
+    cuuint64_t strides[1] = {cuuint64_t(width)};
+    cuuint32_t box[2] = {128u, cuuint32_t(box_rows)};
+    cuuint32_t estr[2] = {1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// How a kv8 decode's query rows are cut: `rows` per pass (both heads' of a pair at D = 64),
+// as few as hold all G * Sq rows of a KV head, 32 at most; then several units.
+constexpr int kKv8MaxCtas = 480;
+struct Kv8Plan {
+    int rows, groups, units;
+    long long items;
+    size_t off_ml, off_o, bytes;  // workspace: item starts, partial sums, partial outputs
+};
+Kv8Plan kv8_plan(int B, int Sq, int Hq, int Hkv, int D) {
+    Kv8Plan pl;
+    const long long sub = (long long)(Hq / Hkv) * Sq;  // rows of one KV head
+    const int heads = D == 64 ? 2 : 1;
+    pl.rows = 4;
+    while (pl.rows < 32 && pl.rows < sub * heads) pl.rows *= 2;
+    pl.groups = (Hkv + heads - 1) / heads;
+    pl.units = int((sub * heads + pl.rows - 1) / pl.rows);
+    pl.items = (long long)B * pl.groups * pl.units;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    pl.off_ml = up(size_t(pl.items + 1) * 8);
+    pl.off_o = pl.off_ml + up(size_t(kKv8MaxCtas) * 2 * pl.rows * 8);
+    pl.bytes = pl.off_o + size_t(kKv8MaxCtas) * 2 * pl.rows * 128 * 4;
+    return pl;
 }
 
 constexpr int kTablesMaxRequests = 16384;  // two ints of shared memory each
@@ -147,8 +188,9 @@ int gqa_attn_kv8_gather(const void* k8, const void* v8, const float* k_scale,
 }
 
 size_t gqa_attn_kv8_decode_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D) {
-    (void)B, (void)Sq, (void)Hq, (void)Hkv, (void)D;
-    return 0;
+    if (B <= 0 || Sq <= 0 || Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || (D != 64 && D != 128))
+        return 0;
+    return kv8_plan(B, Sq, Hq, Hkv, D).bytes;
 }
 
 int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const float* k_scale,
@@ -172,9 +214,9 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
         !aligned(seqlens_k, 4) || !aligned(cu_seqlens_q, 4) || !aligned(lse, 4) ||
         !aligned(workspace, 16))
         return GQA_ERR_ALIGN;
-    if (B > 65535 || Sq > 65535) return GQA_ERR_SHAPE;
-    if (workspace_bytes < gqa_attn_kv8_decode_workspace_bytes(B, Sq, Hq, Hkv, D))
-        return GQA_ERR_WORKSPACE;
+    const Kv8Plan pl = kv8_plan(B, Sq, Hq, Hkv, D);
+    if (pl.items > INT32_MAX) return GQA_ERR_SHAPE;
+    if (!workspace || workspace_bytes < pl.bytes) return GQA_ERR_WORKSPACE;
     DeviceInfo* dev = nullptr;
     rc = device_info(&dev);
     if (rc != GQA_OK) return rc;
@@ -182,31 +224,68 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
-    p.k8 = static_cast<const uint8_t*>(k8);
-    p.v8 = static_cast<const uint8_t*>(v8);
     p.k_scale = k_scale;
     p.v_scale = v_scale;
     p.block_table = block_table;
     p.seqlens_k = seqlens_k;
     p.cu_seqlens_q = cu_seqlens_q;
+    char* ws = static_cast<char*>(workspace);
+    p.meta = reinterpret_cast<long long*>(ws);
+    p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
+    p.part_o = reinterpret_cast<float*>(ws + pl.off_o);
     p.B = B;
     p.Sq = Sq;
     p.total_q = total_q;
     p.Hq = Hq;
     p.Hkv = Hkv;
     p.G = Hq / Hkv;
+    p.groups = pl.groups;
+    p.units = pl.units;
     p.num_pages = num_pages;
     p.page_shift = log2_exact(page_size);
     p.sb_shift = log2_exact(scale_block);
     p.max_pages = max_pages;
     p.window = window;
     p.scale_log2 = scale * kLog2e;
-    const dim3 g(Hq, Sq, B);
-    if (D == 128)
-        gqa::kv8_decode_simple<128><<<g, 128, 0, stream>>>(p);
-    else
-        gqa::kv8_decode_simple<64><<<g, 128, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+    const int box = std::min(page_size, 128);
+    CUtensorMap tk, tv;
+    if (!make_map_kv8(&tk, k8, (long long)num_pages * page_size, Hkv * D, box) ||
+        !make_map_kv8(&tv, v8, (long long)num_pages * page_size, Hkv * D, box))
+        return GQA_ERR_CUDA;
+    // a CTA per tile at most
+    const long long tiles = pl.items * (((long long)max_pages * page_size + 127) / 128);
+    const int sms = dev->sms;
+    auto launch = [&](auto rows, auto pair, int bit) -> int {
+        using C = gqa::Kv8Cfg<rows()>;
+        const int r = ensure_smem_limit(gqa::kv8_decode<rows(), pair()>, 1 << bit, C::SMEM_BYTES);
+        if (r != GQA_OK) return r;
+        p.grid = int(std::min<long long>(tiles, std::min(C::CTAS_PER_SM * sms, kKv8MaxCtas)));
+        gqa::kv8_decode<rows(), pair()><<<p.grid, C::THREADS, C::SMEM_BYTES, stream>>>(tk, tv, p);
+        if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
+        cudaLaunchConfig_t cfg = {};
+        const unsigned y = unsigned(std::min<long long>(pl.items, 65535));
+        cfg.gridDim = dim3(rows(), y, unsigned((pl.items + 65534) / 65535));
+        cfg.blockDim = dim3(128);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, gqa::kv8_combine<rows(), pair()>, p) == cudaSuccess
+                   ? GQA_OK
+                   : GQA_ERR_CUDA;
+    };
+    auto pick = [&](auto pair, int bit) {
+        using std::integral_constant;
+        switch (pl.rows) {
+            case 4: return launch(integral_constant<int, 4>(), pair, bit);
+            case 8: return launch(integral_constant<int, 8>(), pair, bit + 1);
+            case 16: return launch(integral_constant<int, 16>(), pair, bit + 2);
+            default: return launch(integral_constant<int, 32>(), pair, bit + 3);
+        }
+    };
+    return D == 64 ? pick(std::true_type(), 20) : pick(std::false_type(), 24);
 }
 
 }  // extern "C"
