@@ -286,7 +286,10 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         range[0] = 0;
         fence_mbar_init();
     }
-    if (warp == 4) tmem_alloc(tmem_slot, C::TMEM_COLS);
+    if (warp == 4) {
+        tmem_alloc(tmem_slot, C::TMEM_COLS);
+        tmem_relinquish();  // at once: the SM's other CTAs cannot allocate before
+    }
 
     // Every CTA adds up all tiles and finds the item its own range starts in.
     {
@@ -675,7 +678,6 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
     __syncthreads();
     if (warp == 4) {
         tc_fence_after();
-        tmem_relinquish();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
 }
