@@ -19,19 +19,24 @@
 // Scales: a key's K scale multiplies its logit.  Its V scale is folded into its weight,
 // relative to the largest V scale of the tile (vref), which comes back when the tile's
 // O^T is added to the fp32 sum held in registers.  With z the logit in log2 units and
-// d = log2(vs / vref) <= 0, a tile's reference is max_j (z_j + max(d_j, -60)) and the
-// running reference m its maximum over the tiles: weights 2^(z - m) vs / vref stay at or
-// below 1 where they are rounded, and the normaliser's terms 2^(z - m) at or below 2^60,
-// however unlike the scales of neighbouring blocks are.
+// d = log2(vs / vref) <= 0, a row's reference m is at least max_j (z_j + max(d_j, -60)) - 3:
+// weights 32 * 2^(z - m) vs / vref stay at or below 256 where they are rounded, and the
+// normaliser's terms 2^(z - m) at or below 2^63, however unlike the scales of neighbouring
+// blocks are.  The 3 let the reference stay as it is in most tiles: a tile is computed
+// with the last one, every thread checks its own keys, and only where one is above the
+// maximum is taken over all keys (a warp reduction a row, and an exchange) and the tile
+// computed again.
 //
 // Heads of 64 dimensions go in pairs: a 128-byte row holds two KV heads, each query row is
 // padded with zeros in the other's half, and each half of O^T is read by its own head's
 // rows (the MMA's idle half costs nothing here).
 //
-// Work: the (sequence, head group, row unit) items are laid end to end, in tiles of 128
-// keys, and every CTA of a fixed grid takes an equal range of them, whatever the lengths.
-// An item that ends up in several CTAs leaves one fp32 partial in each, joined by
-// kv8_combine, a programmatic dependent launch.
+// Work: the (sequence, row unit) items of one head group are laid end to end, in tiles of
+// 128 keys, and cut into equal ranges, whatever the lengths.  A range is taken by a team
+// of CTAs, one for each head group (`width` of them): they walk the same keys side by
+// side, so that the 128-byte pieces of one token's row are read at about the same time,
+// which is what DRAM wants.  An item that ends up in several ranges leaves one fp32
+// partial in each, joined by kv8_combine, a programmatic dependent launch.
 #pragma once
 #include "kv8_cache.cuh"
 
@@ -46,12 +51,12 @@ struct Kv8DecodeParams {
     const int* block_table;   // [B, max_pages]
     const int* seqlens_k;     // [B]
     const int* cu_seqlens_q;  // [B + 1] or null: Sq queries each
-    float* part_o;            // [grid, 2, R, 128] fp32 partials of a CTA's cut items
-    float2* part_ml;          // [grid, 2, R] reference (log2 units) and sum
-    long long* meta;          // [items]: an item's first tile; [items]: all tiles
+    float* part_o;            // [CTAs, 2, R, 128] fp32 partials of a CTA's cut items
+    float2* part_ml;          // [CTAs, 2, R] reference (log2 units) and sum
+    long long* meta;          // [items]: an item's first tile of its head group's; then: all of them
     int B, Sq, total_q, Hq, Hkv, G;
     int groups, units;        // head groups (KV heads, or pairs of them); row units of each
-    int grid;                 // CTAs of kv8_decode
+    int width, teams;         // CTAs of a team (divides groups), teams of the grid
     int num_pages, page_shift, sb_shift, max_pages, window;
     float scale_log2;
 };
@@ -65,19 +70,24 @@ struct Kv8Cfg {
     static constexpr int OFF_K = 0;
     static constexpr int OFF_V = ST * TILE;
     static constexpr int OFF_Q = 2 * ST * TILE;
-    static constexpr int OFF_P = OFF_Q + N * 128;
-    static constexpr int OFF_SC = OFF_P + N * 128;      // [ST][2 halves][8 groups] float4
+    static constexpr int OFF_P = OFF_Q + N * 128;       // two buffers
+    static constexpr int OFF_SC = OFF_P + 2 * N * 128;      // [ST][2 halves][8 groups] float4
     static constexpr int OFF_VREF = OFF_SC + ST * 256;  // [ST][2]
     static constexpr int OFF_RED = OFF_VREF + ST * 8;   // [4 warps][ROWS]
-    static constexpr int OFF_QF = OFF_RED + 16 * ROWS;  // [ROWS]
-    static constexpr int OFF_BAR = OFF_QF + 4 * ROWS;
-    static constexpr int N_BAR = 5 * ST + 2;
+    static constexpr int OFF_ROW = OFF_RED + 16 * ROWS;  // [ROWS] logit factor, reference
+    static constexpr int OFF_LIM = OFF_ROW + 8 * ROWS;   // [ROWS] keys a row sees: from, to
+    static constexpr int OFF_TOP = OFF_LIM + 8 * ROWS;   // [ROWS] next reference, as ordered int
+    static constexpr int OFF_BAR = OFF_TOP + 4 * ROWS;
+    static constexpr int N_BAR = 5 * ST + 4;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
     static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
-    static constexpr int TMEM_COLS = 2 * N;             // S^T and O^T
+    static constexpr int TMEM_COLS = 4 * N;             // two buffers of S^T and of O^T
     static constexpr int THREADS = 160;
     static constexpr int CTAS_PER_SM = ROWS <= 16 ? 3 : 2;
 };
+
+// Reference of a row that no key has reached: any logit is above it, and it stays finite
+constexpr float kNoKey = -1e30f;
 
 struct Kv8Seq {
     int q0, n, len;  // first query row, queries, keys
@@ -124,7 +134,7 @@ __device__ __forceinline__ Kv8Keys kv8_keys(const Kv8DecodeParams& p, const Kv8S
 // A CTA's walk over its range of tiles: segments of consecutive items.
 template <int SUB>
 struct Kv8Walk {
-    int b, hg, u;        // the item
+    int b, hs, u;        // the item: sequence, set of `width` head groups, row unit
     int off;             // its tiles already passed
     long long left;      // tiles of this CTA still to come
     Kv8Seq seq;
@@ -134,9 +144,9 @@ struct Kv8Walk {
         keys = kv8_keys<SUB>(p, seq, u);
         n = keys.tiles();
     }
-    __device__ __forceinline__ void start(const Kv8DecodeParams& p, int b_, int hg_, int u_,
+    __device__ __forceinline__ void start(const Kv8DecodeParams& p, int b_, int hs_, int u_,
                                           int off_, long long left_) {
-        b = b_, hg = hg_, u = u_, off = off_, left = left_;
+        b = b_, hs = hs_, u = u_, off = off_, left = left_;
         if (left > 0) {
             seq = kv8_seq(p, b);
             load(p);
@@ -152,8 +162,8 @@ struct Kv8Walk {
         do {
             if (++u == p.units) {
                 u = 0;
-                if (++hg == p.groups) {
-                    hg = 0;
+                if (++hs == p.groups / p.width) {
+                    hs = 0;
                     seq = kv8_seq(p, ++b);
                 }
             }
@@ -162,12 +172,20 @@ struct Kv8Walk {
     }
 };
 
-// First tile of CTA `cta` of `ctas` (those with work: a tile each at least)
-__device__ __forceinline__ int kv8_ctas(long long tiles, int grid) {
-    return int(min(tiles, (long long)grid));
+// Teams with work (a tile each at least), and the first tile of one
+__device__ __forceinline__ int kv8_teams(long long tiles, int teams) {
+    return int(min(tiles, (long long)teams));
 }
-__device__ __forceinline__ long long kv8_range_start(long long tiles, int cta, int ctas) {
-    return tiles * cta / ctas;
+__device__ __forceinline__ long long kv8_range_start(long long tiles, int team, int teams) {
+    return tiles * team / teams;
+}
+// float bits as an int that orders like the float, and back
+__device__ __forceinline__ int ordered(float x) {
+    const int i = __float_as_int(x);
+    return i < 0 ? i ^ 0x7fffffff : i;
+}
+__device__ __forceinline__ float unordered(int i) {
+    return __int_as_float(i < 0 ? i ^ 0x7fffffff : i);
 }
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -202,19 +220,23 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, int r0, float w, fl
         f[i] = fmaf(__uint_as_float(C == 8 ? b[i] : a[4 + i]), w, __uint_as_float(a[i]));
 }
 
-// x0, x1 as two e4m3 terms each: hi (bytes: x0, x1) and lo, x = hi + lo / shift
-__device__ __forceinline__ void split_e4m3x2(float x0, float x1, float shift, uint16_t& hi,
-                                             uint16_t& lo) {
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x1), "f"(x0));
-    uint32_t back;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(hi));
-    add_f16x2_to_f32(back ^ 0x80008000u, x0, x1);
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-        : "=h"(lo)
-        : "f"(x1 * shift), "f"(x0 * shift));
+// Four values as two e4m3 terms each (byte i: value i), x = hi + lo / shift
+__device__ __forceinline__ void split_e4m3x4(float x0, float x1, float x2, float x3, float shift,
+                                             uint32_t& hi, uint32_t& lo) {
+    hi = pack_e4m3x4(x0, x1, x2, x3);
+    uint32_t h01, h23;
+    e4m3x4_to_f16x4(hi, h01, h23);
+    add_f16x2_to_f32(h01 ^ 0x80008000u, x0, x1);
+    add_f16x2_to_f32(h23 ^ 0x80008000u, x2, x3);
+    lo = pack_e4m3x4(x0 * shift, x1 * shift, x2 * shift, x3 * shift);
 }
-__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
-    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+// Descriptor of an operand of 16-byte chunks along M or N with no swizzle, the chunks of
+// consecutive k next to each other: kgroup bytes from eight k to the next eight, chunk
+// bytes from one chunk to the next (leading and stride offset of this layout).
+__device__ __forceinline__ uint64_t mn_chunk_desc(uint32_t smem_addr, uint32_t kgroup,
+                                                  uint32_t chunk) {
+    return uint64_t((smem_addr >> 4) & 0x3FFFu) | uint64_t(kgroup >> 4) << 16 |
+           uint64_t(chunk >> 4) << 32 | uint64_t(1) << 46;
 }
 __device__ __forceinline__ float warp_max(float x) {
     float r;
@@ -246,6 +268,24 @@ __device__ __forceinline__ bool kv8_row(const Kv8DecodeParams& p, const Kv8Seq& 
     return i < s.n && kvh < p.Hkv;
 }
 
+// Dimension `dim` (0..127, of both heads of a pair) of a finished row: its sum over the
+// keys of weights (relative to 2^ref) times values, and of weights
+template <int ROWS, bool PAIR>
+__device__ __forceinline__ void kv8_store(const Kv8DecodeParams& p, const Kv8Seq& seq, int b,
+                                          int hg, int u, int r, int dim, float acc, float sum,
+                                          float ref) {
+    constexpr int D = PAIR ? 64 : 128;
+    int i, h;
+    if (!kv8_row<ROWS, PAIR>(p, seq, hg, u, r, i, h)) return;
+    if (!PAIR || dim / 64 == r / (ROWS / 2))
+        p.out[(size_t(seq.q0 + i) * p.Hq + h) * D + (dim & (D - 1))] =
+            __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
+    if (dim == 0)
+        p.lse[p.cu_seqlens_q ? size_t(h) * p.total_q + seq.q0 + i
+                             : (size_t(b) * p.Hq + h) * p.Sq + i] =
+            sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+}
+
 template <int ROWS, bool PAIR>
 __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_SM)
     kv8_decode(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -262,11 +302,11 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
     uint64_t* empty_v = full_v + C::ST;
     uint64_t* full_s = empty_v + C::ST;
     uint64_t* s_done = full_s + C::ST;
-    uint64_t* o_done = s_done + 1;
+    uint64_t* o_done = s_done + 2;
     int* misc = reinterpret_cast<int*>(smem + C::OFF_MISC);
     volatile int* abort_flag = misc;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
-    volatile int* first_item = misc + 2;                                   // b, hg, u, off
+    volatile int* first_item = misc + 2;                                   // b, hs, u, off
     volatile long long* range = reinterpret_cast<volatile long long*>(misc + 6);  // left, first tile
     long long* scan = reinterpret_cast<long long*>(smem + C::OFF_P);       // before P is used
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -280,8 +320,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             mbar_init(empty_v + s, 1);
             mbar_init(full_s + s, 1);
         }
-        mbar_init(s_done, 1);
-        mbar_init(o_done, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(s_done + i, 1);
         *abort_flag = 0;
         range[0] = 0;
         fence_mbar_init();
@@ -291,18 +330,20 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         tmem_relinquish();  // at once: the SM's other CTAs cannot allocate before
     }
 
-    // Every CTA adds up all tiles and finds the item its own range starts in.
+    // Every CTA adds up the tiles of one head group and finds the item its range starts in.
+    const int team = blockIdx.x / p.width, member = blockIdx.x - team * p.width;
     {
+        const int sets = p.groups / p.width;
         const int per = (p.B + C::THREADS - 1) / C::THREADS;
         const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-        auto tiles_of = [&](int b) {  // of one head group
+        auto tiles_of = [&](int b) {
             const Kv8Seq s = kv8_seq(p, b);
             long long t = 0;
             for (int u = 0; u < p.units; ++u) t += kv8_keys<SUB>(p, s, u).tiles();
             return t;
         };
         long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += tiles_of(b) * p.groups;
+        for (int b = b0; b < b1; ++b) mine += tiles_of(b) * sets;
         long long inc = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -316,21 +357,21 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             if (w < warp) before += scan[w];
             all += scan[w];
         }
-        const int ctas = kv8_ctas(all, p.grid);
-        const bool works = int(blockIdx.x) < ctas;
-        const long long lo = works ? kv8_range_start(all, blockIdx.x, ctas) : 0;
-        const long long hi = works ? kv8_range_start(all, blockIdx.x + 1, ctas) : 0;
+        const int teams = kv8_teams(all, p.teams);
+        const bool works = team < teams;
+        const long long lo = works ? kv8_range_start(all, team, teams) : 0;
+        const long long hi = works ? kv8_range_start(all, team + 1, teams) : 0;
         if (blockIdx.x == 0 && tid == 0) p.meta[(long long)p.B * p.groups * p.units] = all;
         if (lo < hi && lo >= before && lo < before + mine) {
             long long at = lo - before;
             int b = b0;
             long long t = tiles_of(b);
-            while (at >= t * p.groups) {
-                at -= t * p.groups;
+            while (at >= t * sets) {
+                at -= t * sets;
                 t = tiles_of(++b);
             }
-            const int hg = int(at / t);
-            at -= hg * t;
+            const int hs = int(at / t);
+            at -= hs * t;
             const Kv8Seq s = kv8_seq(p, b);
             int u = 0, n = kv8_keys<SUB>(p, s, 0).tiles();
             while (at >= n) {
@@ -338,7 +379,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 n = kv8_keys<SUB>(p, s, ++u).tiles();
             }
             first_item[0] = b;
-            first_item[1] = hg;
+            first_item[1] = hs;
             first_item[2] = u;
             first_item[3] = int(at);
             range[0] = hi - lo;
@@ -368,8 +409,9 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         bool ok = true;
         for (; walk.left > 0 && ok; walk.next(p)) {
             const int* row = p.block_table + size_t(walk.b) * p.max_pages;
-            const int x = walk.hg * 128;
-            const int kvh = PAIR ? 2 * walk.hg + half : walk.hg;
+            const int hg = walk.hs * p.width + member;
+            const int x = hg * 128;
+            const int kvh = PAIR ? 2 * hg + half : hg;
             const bool here = lane < (PAIR ? 16 : 8) && kvh < p.Hkv;
             const int t1 = walk.keys.first() + walk.off + walk.segment();
             for (int t = walk.keys.first() + walk.off; t < t1 && ok; ++t, ++c) {
@@ -423,10 +465,10 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 const float rel = vref > 0.f ? vs / vref : 0.f;
                 if (lane < 16)
                     reinterpret_cast<float4*>(smem + C::OFF_SC)[s * 16 + lane] =
-                        make_float4(ks, fmaxf(__log2f(rel), -60.f), rel * 128.f, 0.f);
+                        make_float4(ks, fmaxf(__log2f(rel), -60.f), rel * 32.f, 0.f);
                 if (lane < 16 && grp == 0)
                     reinterpret_cast<float*>(smem + C::OFF_VREF)[s * 2 + half] =
-                        vref * 0.0078125f;
+                        vref * 0.03125f;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full_s + s);
             }
@@ -448,29 +490,33 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
     } else {
         // ------------------------------------------------------------ consumers
         const uint32_t idesc_s = idesc_e4m3_f32(128, C::N, 0, 0);
-        const uint32_t idesc_o = idesc_e4m3_f32(128, C::N, 1, 0);
+        const uint32_t idesc_o = idesc_e4m3_f32(128, C::N, 1, 1);
         const uint64_t dk = sw128_desc(smem_u32(smem + C::OFF_K), 16, 1024);
         const uint64_t dv = sw128_desc(smem_u32(smem + C::OFF_V), C::TILE, 1024);
         const uint64_t dq = sw128_desc(smem_u32(smem + C::OFF_Q), 16, 1024);
-        const uint64_t dp = sw128_desc(smem_u32(smem + C::OFF_P), 16, 1024);
+        // P: [N / 16 chunks][128 keys][16 columns], so a thread stores its key's columns whole
+        const uint64_t dp = mn_chunk_desc(smem_u32(smem + C::OFF_P), 128, 2048);
+        const uint32_t sp = smem_u32(smem + C::OFF_P) + tid * 16;
         const uint32_t lane_base = uint32_t(warp * 32) << 16;  // this warp's TMEM lanes
-        const uint32_t t_s = tmem + lane_base, t_o = t_s + C::N;
+        const uint32_t t_s = tmem + lane_base, t_o = t_s + 2 * C::N;
         const uint32_t sq = smem_u32(smem + C::OFF_Q);
-        // this thread's key column of P (row r: + r * 128, chunk xor r & 7)
-        const uint32_t sp = smem_u32(smem + C::OFF_P) + (tid & 15);
         float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
-        float* qf = reinterpret_cast<float*>(smem + C::OFF_QF);
+        float2* rows = reinterpret_cast<float2*>(smem + C::OFF_ROW);
+        int2* limits = reinterpret_cast<int2*>(smem + C::OFF_LIM);
+        int* next_ref = reinterpret_cast<int*>(smem + C::OFF_TOP);
+        float* so = reinterpret_cast<float*>(smem + C::OFF_P);  // [ROWS][128], P unused
         const int my_half = PAIR ? tid >> 6 : 0;  // of this thread's dimension
         int c = 0;
         bool aborted = false, first_segment = true;
         for (; walk.left > 0; walk.next(p), first_segment = false) {
+            const int hg = walk.hs * p.width + member;
             const int segment = walk.segment();
             const bool whole = walk.off == 0 && segment == walk.n;
             // --- q rows of this item as two e4m3 terms; the MMAs that read the last
             // item's rows have completed
             for (int r = warp; r < ROWS; r += 4) {
                 int i, h;
-                const bool valid = kv8_row<ROWS, PAIR>(p, walk.seq, walk.hg, walk.u, r, i, h);
+                const bool valid = kv8_row<ROWS, PAIR>(p, walk.seq, hg, walk.u, r, i, h);
                 constexpr int D = PAIR ? 64 : 128;
                 const int d0 = PAIR ? (lane * 4) & 63 : lane * 4;
                 const bool in = valid && (!PAIR || (lane >> 4) == r / SUB);
@@ -484,31 +530,35 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 // power-of-two factor that brings the row's largest |q| to [128, 256)
                 const int e = max(int(amax >> 23), 8);
                 const float up = __uint_as_float(uint32_t(261 - e) << 23);
-                uint16_t hi[2], lo[2];
-                split_e4m3x2(bf16_lo(w.x) * up, bf16_hi(w.x) * up, 16.f, hi[0], lo[0]);
-                split_e4m3x2(bf16_lo(w.y) * up, bf16_hi(w.y) * up, 16.f, hi[1], lo[1]);
-                const uint32_t at = (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-                const uint32_t row_hi = sq + r * 128 + at;
-                const uint32_t row_lo = sq + (ROWS + r) * 128 +
-                                        (((lane >> 2) ^ ((ROWS + r) & 7)) << 4) + (lane & 3) * 4;
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(row_hi),
-                             "r"(uint32_t(hi[0]) | uint32_t(hi[1]) << 16)
-                             : "memory");
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(row_lo),
-                             "r"(uint32_t(lo[0]) | uint32_t(lo[1]) << 16)
-                             : "memory");
+                uint32_t hi, lo;
+                split_e4m3x4(bf16_lo(w.x) * up, bf16_hi(w.x) * up, bf16_lo(w.y) * up,
+                             bf16_hi(w.y) * up, 16.f, hi, lo);
+                auto put = [&](int n, uint32_t codes) {  // row n of the operand, this lane's dims
+                    const uint32_t at = (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4;
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(sq + n * 128 + at), "r"(codes)
+                                 : "memory");
+                };
+                put(r, hi);
+                put(ROWS + r, lo);
                 // a row with an infinity or a NaN has no factor: its logits are NaN
-                if (lane == 0)
-                    qf[r] = amax >= 0x7f800000u ? NAN
-                                                : __uint_as_float(uint32_t(e - 7) << 23) *
-                                                      p.scale_log2;
+                if (lane == 0) {
+                    const int end = walk.seq.len - walk.seq.n + i + 1;
+                    limits[r] = make_int2(p.window > 0 ? end - p.window : 0,
+                                          min(end, walk.keys.hi));
+                    next_ref[r] = ordered(kNoKey);
+                    rows[r] = make_float2(
+                        amax >= 0x7f800000u
+                            ? NAN
+                            : __uint_as_float(uint32_t(e - 7) << 23) * p.scale_log2,
+                        kNoKey);
+                }
             }
             fence_proxy_async();
             consumers_sync();
 
-            float m[ROWS], l[ROWS], o[ROWS];
+            float l[ROWS], o[ROWS];
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) m[r] = -INFINITY, l[r] = 0.f, o[r] = 0.f;
+            for (int r = 0; r < ROWS; ++r) l[r] = 0.f, o[r] = 0.f;
             // keys that every row sees, in tiles between which no mask is needed
             const int t0 = walk.keys.first() + walk.off;
             const int last = walk.seq.len - walk.seq.n;  // position of query 0
@@ -516,21 +566,49 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             const int i_hi = min((walk.u * SUB + SUB - 1) / p.G, walk.seq.n - 1);
             const int all_hi = last + i_lo + 1;
             const int all_lo = p.window > 0 ? max(last + i_hi + 1 - p.window, 0) : 0;
-            for (int t = t0; t < t0 + segment && !aborted; ++t, ++c) {
+            // S^T of tile x (counted over the CTA) into its buffer
+            auto issue_s = [&](int x) {
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_ss_f8(tmem + (x & 1) * C::N,
+                               dk + (((x % C::ST) * C::TILE + kk * 32) >> 4),
+                               dq + ((kk * 32) >> 4), idesc_s, kk > 0);
+                umma_commit(empty_k + x % C::ST);
+                umma_commit(s_done + (x & 1));
+            };
+            int s_next = c;          // thread 0: the first tile whose S^T is not issued
+            bool pending = false;    // the O^T of tile c - 1 is not in o yet
+            float vref_pending = 0.f;
+            const int c_end = c + segment;
+            auto issue_ahead = [&](int x) {  // tile x, if its keys are here
+                if (s_next == x && x < c_end && mbar_try_wait(full_k + x % C::ST, (x / C::ST) & 1)) {
+                    issue_s(x);
+                    ++s_next;
+                }
+            };
+            // adds the pending O^T
+            auto take_o = [&](int x) {
+                mbar_wait_warp(o_done + (x & 1), (x >> 1) & 1, abort_flag);
+                tc_fence_after();
+#pragma unroll
+                for (int r0 = 0; r0 < ROWS; r0 += CH) {
+                    float f[CH];
+                    tmem_ld_rows<ROWS, CH>(t_o + (x & 1) * C::N, r0, 0.03125f, f);
+#pragma unroll
+                    for (int j = 0; j < CH; ++j) o[r0 + j] = fmaf(f[j], vref_pending, o[r0 + j]);
+                }
+                tc_fence_before();
+                pending = false;
+            };
+            for (int t = t0; t < t0 + segment; ++t, ++c) {
                 const int s = c % C::ST;
                 const uint32_t ph = (c / C::ST) & 1;
                 bool ok = true;
-                if (tid == 0) {
+                if (tid == 0 && s_next == c) {
                     ok = mbar_wait(full_k + s, ph, abort_flag);
-                    if (ok) {
-                        tc_fence_after();
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_ss_f8(tmem, dk + ((s * C::TILE + kk * 32) >> 4),
-                                       dq + ((kk * 32) >> 4), idesc_s, kk > 0);
-                        umma_commit(empty_k + s);
-                        umma_commit(s_done);
-                    }
+                    if (ok) issue_s(c);
+                    ++s_next;
                 }
                 __syncwarp();
                 const int key = t * 128 + tid;
@@ -541,58 +619,27 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     sc[1] = reinterpret_cast<float4*>(smem + C::OFF_SC)[s * 16 + 8 + (tid >> 4)];
                 const float vref =
                     reinterpret_cast<float*>(smem + C::OFF_VREF)[s * 2 + my_half];
-                ok &= mbar_wait_warp(s_done, c & 1, abort_flag);
+                ok &= mbar_wait_warp(s_done + (c & 1), (c >> 1) & 1, abort_flag);
                 tc_fence_after();
+                if (tid == 0) issue_ahead(c + 1);
+                __syncwarp();
                 const bool edge = t * 128 < all_lo || t * 128 + 128 > all_hi;
-                float z[ROWS];
-                float top = -INFINITY;  // lane r: the warp's largest z + d of row r
+                const uint32_t t_sc = t_s + (c & 1) * C::N;
+                const uint32_t sp_c = sp + (c & 1) * (C::N * 128);
+                // logits of rows r0 .. r0 + CH - 1 in log2 units, -inf where not seen
+                auto logits = [&](int r0, float (&f)[CH]) {
+                    tmem_ld_rows<ROWS, CH>(t_sc, r0, 0.0625f, f);
 #pragma unroll
-                for (int r0 = 0; r0 < ROWS; r0 += CH) {
-                    float f[CH];
-                    tmem_ld_rows<ROWS, CH>(t_s, r0, 0.0625f, f);
+                    for (int j = 0; j < CH; ++j)
+                        f[j] *= sc[PAIR ? (r0 + j) / SUB : 0].x * rows[r0 + j].x;
+                    if (edge) {
 #pragma unroll
-                    for (int j = 0; j < CH; ++j) {
-                        const int r = r0 + j;
-                        const float4& k = sc[PAIR ? r / SUB : 0];
-                        z[r] = f[j] * (k.x * qf[r]);
-                        if (edge) {
-                            const int i = (walk.u * SUB + r % SUB) / p.G;
-                            const int hi = min(last + i + 1, walk.keys.hi);
-                            if (key >= hi || (p.window > 0 && key < last + i + 1 - p.window))
-                                z[r] = -INFINITY;
+                        for (int j = 0; j < CH; ++j) {
+                            const int2 lim = limits[r0 + j];
+                            if (key < lim.x || key >= lim.y) f[j] = -INFINITY;
                         }
-                        const float mx = warp_max(z[r] + k.y);
-                        if (lane == r) top = mx;
                     }
-                }
-                if (lane < ROWS) red[warp * ROWS + lane] = top;
-                consumers_sync();
-#pragma unroll
-                for (int r = 0; r < ROWS; r += 2) {
-                    float w[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int a = r + j;
-                        const float mt = fmaxf(fmaxf(red[a], red[ROWS + a]),
-                                               fmaxf(red[2 * ROWS + a], red[3 * ROWS + a]));
-                        const float m1 = fmaxf(m[a], mt);
-                        const float mu = m1 == -INFINITY ? 0.f : m1;
-                        const float alpha = ex2_approx(m[a] - mu);
-                        const float u = ex2_approx(z[a] - mu);
-                        m[a] = m1;
-                        l[a] = fmaf(l[a], alpha, u);
-                        o[a] *= alpha;
-                        w[j] = u * sc[PAIR ? a / SUB : 0].z;
-                    }
-                    uint16_t hi, lo;
-                    split_e4m3x2(w[0], w[1], 32.f, hi, lo);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int a = r + j, b = ROWS + r + j;
-                        st_shared_u8(sp + a * 128 + (((tid >> 4) ^ (a & 7)) << 4), hi >> (8 * j));
-                        st_shared_u8(sp + b * 128 + (((tid >> 4) ^ (b & 7)) << 4), lo >> (8 * j));
-                    }
-                }
+                };
                 // V rows that no query sees may hold any code: a weight of 0 times NaN
                 // would still reach O
                 if (t * 128 < walk.keys.lo || t * 128 + 128 > walk.keys.hi) {
@@ -603,34 +650,97 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                         for (int j = 0; j < 8; ++j) st_shared_v4(v + j * 16, 0u, 0u, 0u, 0u);
                     }
                 }
-                fence_proxy_async();
-                tc_fence_before();
-                aborted = consumers_any(!ok);
-                if (tid == 0 && !aborted) {
-                    ok = mbar_wait(full_v + s, ph, abort_flag);
-                    if (ok) {
+                // the weights relative to the rows' references: their terms u, and P
+                float u[ROWS];
+                for (int pass = 0;; ++pass) {
+                    bool high = pass == 0;
+                    if (pass > 0 || t > t0) {
+                        uint32_t codes[C::N / 4];  // hi of every row, then lo
+                        float above[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                        for (int i = 0; i < C::N / 4; ++i) codes[i] = 0u;
+#pragma unroll
+                        for (int r0 = 0; r0 < ROWS; r0 += CH) {
+                            float f[CH];
+                            logits(r0, f);
+#pragma unroll
+                            for (int j = 0; j < CH; j += 4) {
+                                float w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int r = r0 + j + e, half = PAIR ? r / SUB : 0;
+                                    const float x = f[j + e] - rows[r].y;
+                                    above[half] = fmaxf(above[half], x);
+                                    u[r] = ex2_approx(x);
+                                    w[e] = u[r] * sc[half].z;
+                                }
+                                split_e4m3x4(w[0], w[1], w[2], w[3], 32.f, codes[(r0 + j) / 4],
+                                             codes[(ROWS + r0 + j) / 4]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < C::N / 16; ++i)
+                            st_shared_v4(sp_c + i * 2048, codes[4 * i], codes[4 * i + 1],
+                                         codes[4 * i + 2], codes[4 * i + 3]);
+                        // (the second pass has its tile's own references)
+                        high = pass == 0 && (above[0] + sc[0].y > 3.f ||
+                                             (PAIR && above[1] + sc[PAIR ? 1 : 0].y > 3.f));
+                    }
+                    if (__any_sync(0xffffffffu, high)) {
+                        float top = -INFINITY;  // lane r: the warp's largest z + d of row r
+#pragma unroll
+                        for (int r0 = 0; r0 < ROWS; r0 += CH) {
+                            float f[CH];
+                            logits(r0, f);
+#pragma unroll
+                            for (int j = 0; j < CH; ++j) {
+                                const int r = r0 + j;
+                                const float mx = warp_max(f[j] + sc[PAIR ? r / SUB : 0].y);
+                                if (lane == r) top = mx;
+                            }
+                        }
+                        if (lane < ROWS) atomicMax(next_ref + lane, ordered(top));
+                    }
+                    fence_proxy_async();
+                    tc_fence_before();
+                    if (!consumers_any(high || !ok)) break;
+                    aborted = consumers_any(!ok);
+                    if (aborted) break;
+                    if (pending) take_o(c - 1);
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r) {
+                        const float alpha = ex2_approx(rows[r].y - unordered(next_ref[r]));
+                        l[r] *= alpha;
+                        o[r] *= alpha;
+                    }
+                    consumers_sync();
+                    if (tid < ROWS) rows[tid].y = unordered(next_ref[tid]);
+                    consumers_sync();
+                }
+                if (aborted) break;
+                if (tid == 0) {
+                    if (mbar_wait(full_v + s, ph, abort_flag)) {
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_ss_f8(tmem + C::N, dv + ((s * C::TILE + kk * 32 * 128) >> 4),
-                                       dp + ((kk * 32) >> 4), idesc_o, kk > 0);
+                            umma_ss_f8(tmem + (2 + (c & 1)) * C::N,
+                                       dv + ((s * C::TILE + kk * 32 * 128) >> 4),
+                                       dp + (((c & 1) * (C::N * 128) + kk * 512) >> 4), idesc_o,
+                                       kk > 0);
                         umma_commit(empty_v + s);
-                        umma_commit(o_done);
+                        umma_commit(o_done + (c & 1));
                     }
+                    issue_ahead(c + 1);
                 }
                 __syncwarp();
-                // (a wait that runs out here shows in the next tile's waits, or below)
-                mbar_wait_warp(o_done, c & 1, abort_flag);
-                tc_fence_after();
 #pragma unroll
-                for (int r0 = 0; r0 < ROWS; r0 += CH) {
-                    float f[CH];
-                    tmem_ld_rows<ROWS, CH>(t_o, r0, 0.03125f, f);
-#pragma unroll
-                    for (int j = 0; j < CH; ++j) o[r0 + j] = fmaf(f[j], vref, o[r0 + j]);
-                }
-                tc_fence_before();
+                for (int r = 0; r < ROWS; ++r) l[r] += u[r];
+                // (a wait that runs out here shows in the next tile's, or below)
+                if (pending) take_o(c - 1);
+                pending = true;
+                vref_pending = vref;
             }
+            if (pending) take_o(c - 1);
             // --- end of the segment: sums over the keys, then the rows' results
             aborted = consumers_any(aborted || *abort_flag != 0);
 #pragma unroll
@@ -639,39 +749,28 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 for (int off = 16; off > 0; off >>= 1)
                     l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
                 if (lane == 0) red[warp * ROWS + r] = l[r];
+                so[r * 128 + tid] = o[r];  // (read back by this thread)
             }
             consumers_sync();
-            const long long item = ((long long)walk.b * p.groups + walk.hg) * p.units + walk.u;
+            const long long item = ((long long)walk.b * p.groups + hg) * p.units + walk.u;
             const size_t part = size_t(blockIdx.x) * 2 + (first_segment ? 0 : 1);
-#pragma unroll
+#pragma unroll 1
             for (int r = 0; r < ROWS; ++r) {
                 float sum = (red[r] + red[ROWS + r]) + (red[2 * ROWS + r] + red[3 * ROWS + r]);
-                if (aborted) {
-                    // a wait gave up (device error word set): an empty result, so that no
-                    // stale memory is picked up
-                    sum = 0.f, m[r] = -INFINITY, o[r] = 0.f;
-                }
+                float acc = so[r * 128 + tid];
+                // a wait gave up (device error word set): an empty result, so that no stale
+                // memory is picked up
+                if (aborted) sum = 0.f, acc = 0.f;
                 if (!whole) {
-                    p.part_o[(part * ROWS + r) * 128 + tid] = o[r];
-                    if (tid == 0) p.part_ml[part * ROWS + r] = make_float2(m[r], sum);
-                    continue;
-                }
-                int i, h;
-                if (!kv8_row<ROWS, PAIR>(p, walk.seq, walk.hg, walk.u, r, i, h)) continue;
-                const size_t q_row = size_t(walk.seq.q0 + i) * p.Hq + h;
-                const float v = sum == 0.f ? 0.f : o[r] / sum;
-                if constexpr (PAIR) {
-                    if (my_half == r / SUB) p.out[q_row * 64 + (tid & 63)] = __float2bfloat16_rn(v);
+                    p.part_o[(part * ROWS + r) * 128 + tid] = acc;
+                    if (tid == 0) p.part_ml[part * ROWS + r] = make_float2(rows[r].y, sum);
                 } else {
-                    p.out[q_row * 128 + tid] = __float2bfloat16_rn(v);
+                    kv8_store<ROWS, PAIR>(p, walk.seq, walk.b, hg, walk.u, r, tid, acc, sum,
+                                          rows[r].y);
                 }
-                if (tid == 0)
-                    p.lse[p.cu_seqlens_q ? size_t(h) * p.total_q + walk.seq.q0 + i
-                                         : (size_t(walk.b) * p.Hq + h) * p.Sq + i] =
-                        sum == 0.f ? -INFINITY : (m[r] + __log2f(sum)) * 0.69314718055994531f;
             }
             if (tid == 0 && walk.off == 0) p.meta[item] = range[1] + (range[0] - walk.left);
-            consumers_sync();  // red is free again
+            consumers_sync();  // red, rows and P are free again
         }
     }
     tc_fence_before();
@@ -682,13 +781,15 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
     }
 }
 
-// One CTA per (row, item): joins the partials of an item that several CTAs shared, and
+// One CTA per (row, item): joins the partials of an item that several teams shared, and
 // writes the rows that no key reached.  With reference M = max_s m_s (log2 units):
 // sum = sum_s 2^(m_s - M) sum_s, O = sum_s 2^(m_s - M) O_s / sum, L = ln 2 (M + log2 sum).
 template <int ROWS, bool PAIR>
 __global__ void __launch_bounds__(128) kv8_combine(const Kv8DecodeParams p) {
     constexpr int SUB = PAIR ? ROWS / 2 : ROWS;
-    const int r = blockIdx.x, tid = threadIdx.x;
+    __shared__ float factor[480];  // of each partial (at most one a CTA)
+    __shared__ float red[2][4];
+    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const long long item = blockIdx.y + (long long)blockIdx.z * 65535;
     const long long items = (long long)p.B * p.groups * p.units;
     if (item >= items) return;
@@ -699,37 +800,40 @@ __global__ void __launch_bounds__(128) kv8_combine(const Kv8DecodeParams p) {
     int i, h;
     if (!kv8_row<ROWS, PAIR>(p, seq, hg, u, r, i, h)) return;
     const int n = kv8_keys<SUB>(p, seq, u).tiles();
-    const int half = PAIR ? r / SUB : 0;
     griddep_wait();
-    float M = -INFINITY, sum = 0.f, acc = 0.f;
+    float M = kNoKey, sum = 0.f, acc = 0.f;
     if (n > 0) {
         const long long all = p.meta[items], first = p.meta[item];
-        const int ctas = kv8_ctas(all, p.grid);
-        const int c0 = int(((first + 1) * ctas - 1) / all);
-        const int c1 = int(((first + n) * ctas - 1) / all);
+        const int teams = kv8_teams(all, p.teams);
+        const int c0 = int(((first + 1) * teams - 1) / all);
+        const int c1 = int(((first + n) * teams - 1) / all);
         if (c0 == c1) return;  // one CTA has written it
-        // the first CTA's share is its second partial unless its range starts there
-        const bool cut = kv8_range_start(all, c0, ctas) != first;
-        auto part = [&](int c) { return size_t(c) * 2 + (c == c0 && cut ? 1 : 0); };
-        for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.part_ml[part(c) * ROWS + r].x);
-        for (int c = c0; c <= c1; ++c) {
-            const float2 ml = p.part_ml[part(c) * ROWS + r];
-            const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+        // the first team's share is its second partial unless its range starts there
+        const bool cut = kv8_range_start(all, c0, teams) != first;
+        const int member = hg % p.width, parts = c1 - c0 + 1;
+        auto part = [&](int x) {  // partial x of the item, its row r
+            return (size_t((c0 + x) * p.width + member) * 2 + (x == 0 && cut ? 1 : 0)) * ROWS + r;
+        };
+        for (int x = tid; x < parts; x += 128) M = fmaxf(M, p.part_ml[part(x)].x);
+        M = warp_max(M);
+        if (lane == 0) red[0][warp] = M;
+        __syncthreads();
+        M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+        for (int x = tid; x < parts; x += 128) {
+            const float2 ml = p.part_ml[part(x)];
+            const float f = exp2f(ml.x - M);
+            factor[x] = f;
             sum += f * ml.y;
-            acc += f * p.part_o[(part(c) * ROWS + r) * 128 + tid];
         }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0) red[1][warp] = sum;
+        __syncthreads();
+        sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+#pragma unroll 8
+        for (int x = 0; x < parts; ++x) acc += factor[x] * p.part_o[part(x) * 128 + tid];
     }
-    const size_t q_row = size_t(seq.q0 + i) * p.Hq + h;
-    const float v = sum == 0.f ? 0.f : acc / sum;
-    if constexpr (PAIR) {
-        if (tid >> 6 == half) p.out[q_row * 64 + (tid & 63)] = __float2bfloat16_rn(v);
-    } else {
-        p.out[q_row * 128 + tid] = __float2bfloat16_rn(v);
-    }
-    if (tid == 0)
-        p.lse[p.cu_seqlens_q ? size_t(h) * p.total_q + seq.q0 + i
-                             : (size_t(b) * p.Hq + h) * p.Sq + i] =
-            sum == 0.f ? -INFINITY : (M + log2f(sum)) * 0.69314718055994531f;
+    kv8_store<ROWS, PAIR>(p, seq, b, hg, u, r, tid, acc, sum, M);
 }
 
 }  // namespace gqa

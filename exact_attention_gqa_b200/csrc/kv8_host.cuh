@@ -252,15 +252,21 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
     if (!make_map_kv8(&tk, k8, (long long)num_pages * page_size, Hkv * D, box) ||
         !make_map_kv8(&tv, v8, (long long)num_pages * page_size, Hkv * D, box))
         return GQA_ERR_CUDA;
-    // a CTA per tile at most
-    const long long tiles = pl.items * (((long long)max_pages * page_size + 127) / 128);
     const int sms = dev->sms;
     auto launch = [&](auto rows, auto pair, int bit) -> int {
         using C = gqa::Kv8Cfg<rows()>;
         const int r = ensure_smem_limit(gqa::kv8_decode<rows(), pair()>, 1 << bit, C::SMEM_BYTES);
         if (r != GQA_OK) return r;
-        p.grid = int(std::min<long long>(tiles, std::min(C::CTAS_PER_SM * sms, kKv8MaxCtas)));
-        gqa::kv8_decode<rows(), pair()><<<p.grid, C::THREADS, C::SMEM_BYTES, stream>>>(tk, tv, p);
+        // a team's CTAs: as many head groups as divide them all, 16 at most; a team per
+        // tile of one head group at most
+        p.width = std::min(pl.groups, 16);
+        while (pl.groups % p.width) --p.width;
+        const long long tiles = pl.items / p.width *
+                                (((long long)max_pages * page_size + 127) / 128);
+        p.teams = int(std::min<long long>(
+            tiles, std::min(C::CTAS_PER_SM * sms, kKv8MaxCtas) / p.width));
+        const int grid = p.teams * p.width;
+        gqa::kv8_decode<rows(), pair()><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(tk, tv, p);
         if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
         cudaLaunchConfig_t cfg = {};
         const unsigned y = unsigned(std::min<long long>(pl.items, 65535));
