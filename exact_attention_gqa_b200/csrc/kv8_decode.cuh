@@ -17,15 +17,15 @@
 // The terms are further columns of the same MMA, whose N side has room.
 //
 // Scales: a key's K scale multiplies its logit.  Its V scale is folded into its weight,
-// relative to the largest V scale of the tile (vref), which comes back when the tile's
-// O^T is added to the fp32 sum held in registers.  With z the logit in log2 units and
-// d = log2(vs / vref) <= 0, a row's reference m is at least max_j (z_j + max(d_j, -60)) - 3:
-// weights 32 * 2^(z - m) vs / vref stay at or below 256 where they are rounded, and the
+// relative to the largest V scale met so far (vrun), so that O^T can stay in tensor memory
+// and be summed there by the MMA.  With z the logit in log2 units and d = log2(vs / vrun),
+// a row's reference m is kept at or above max_j (z_j + max(d_j, -60)) - 3: weights
+// 32 * 2^(z - m) vs / vrun stay at or below 256 where they are rounded, and the
 // normaliser's terms 2^(z - m) at or below 2^63, however unlike the scales of neighbouring
-// blocks are.  The 3 let the reference stay as it is in most tiles: a tile is computed
-// with the last one, every thread checks its own keys, and only where one is above the
-// maximum is taken over all keys (a warp reduction a row, and an exchange) and the tile
-// computed again.
+// blocks are.  The 3 let references and vrun stay as they are in most tiles: a tile is
+// computed with the last ones, every thread checks its own keys, and only where one is
+// above the maxima are taken over all keys (a warp reduction a row, and an exchange), what
+// is summed so far is rescaled and the tile computed again.
 //
 // Heads of 64 dimensions go in pairs: a 128-byte row holds two KV heads, each query row is
 // padded with zeros in the other's half, and each half of O^T is read by its own head's
@@ -64,26 +64,32 @@ struct Kv8DecodeParams {
 // ROWS query rows (query head x position, of both heads of a pair) per CTA and pass
 template <int ROWS>
 struct Kv8Cfg {
+    static constexpr int WGS = ROWS >= 16 ? 2 : 1;      // consumer warpgroups, rows split
+    static constexpr int RW = ROWS / WGS;               // rows of each
+    static constexpr int CTAS_PER_SM = 2;
+    static constexpr int ST = ROWS <= 16 ? 3 : 2;       // stages: what fits shared memory
     static constexpr int TILE = 128 * 128;              // bytes of K or V per stage
-    static constexpr int ST = 2;                        // stages of each
     static constexpr int N = ROWS <= 8 ? 16 : 2 * ROWS;  // MMA columns: hi and lo of each row
     static constexpr int OFF_K = 0;
     static constexpr int OFF_V = ST * TILE;
     static constexpr int OFF_Q = 2 * ST * TILE;
     static constexpr int OFF_P = OFF_Q + N * 128;       // two buffers
-    static constexpr int OFF_SC = OFF_P + 2 * N * 128;      // [ST][2 halves][8 groups] float4
+    static constexpr int OFF_SC = OFF_P + 2 * N * 128;  // [ST][2 halves][8 groups] float4
     static constexpr int OFF_VREF = OFF_SC + ST * 256;  // [ST][2]
-    static constexpr int OFF_RED = OFF_VREF + ST * 8;   // [4 warps][ROWS]
+    static constexpr int OFF_RED = OFF_VREF + 32;       // [ROWS][4 warps]
     static constexpr int OFF_ROW = OFF_RED + 16 * ROWS;  // [ROWS] logit factor, reference
     static constexpr int OFF_LIM = OFF_ROW + 8 * ROWS;   // [ROWS] keys a row sees: from, to
     static constexpr int OFF_TOP = OFF_LIM + 8 * ROWS;   // [ROWS] next reference, as ordered int
-    static constexpr int OFF_BAR = OFF_TOP + 4 * ROWS;
-    static constexpr int N_BAR = 5 * ST + 4;
+    static constexpr int OFF_VRUN = OFF_TOP + 4 * ROWS;  // [2 halves] vrun, its log2, 1 / vrun
+    static constexpr int OFF_BAR = OFF_VRUN + 32;
+    static constexpr int N_BAR = 5 * ST + 3;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
     static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
-    static constexpr int TMEM_COLS = 4 * N;             // two buffers of S^T and of O^T
-    static constexpr int THREADS = 160;
-    static constexpr int CTAS_PER_SM = ROWS <= 16 ? 3 : 2;
+    static constexpr int TMEM_COLS = N == 16 ? 64 : 4 * N;  // two of S^T, one of O^T
+    static constexpr int CONSUMERS = 128 * WGS;
+    static constexpr int THREADS = CONSUMERS + 64;      // and the producer's and the MMA warp
+    static_assert((SMEM_BYTES + 1024) * CTAS_PER_SM <= 228 * 1024, "shared memory of an SM");
+    static_assert(TMEM_COLS * CTAS_PER_SM <= 512, "tensor memory of an SM");
 };
 
 // Reference of a row that no key has reached: any logit is above it, and it stays finite
@@ -205,9 +211,10 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
         : "memory");
 }
 // Rows [r0, r0 + C) of an accumulator whose column r is row r's hi term and column ROWS + r
-// its lo term: f = hi + lo * w.
+// its lo term.
 template <int ROWS, int C>
-__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, int r0, float w, float (&f)[C]) {
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, int r0, float (&hi)[C],
+                                             float (&lo)[C]) {
     static_assert((ROWS == 4 && C == 4) || C == 8, "");
     uint32_t a[8], b[8];
     tmem_ld8(taddr + r0, a);
@@ -216,10 +223,37 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, int r0, float w, fl
     reg_fence(a);
     if constexpr (C == 8) reg_fence(b);
 #pragma unroll
-    for (int i = 0; i < C; ++i)
-        f[i] = fmaf(__uint_as_float(C == 8 ? b[i] : a[4 + i]), w, __uint_as_float(a[i]));
+    for (int i = 0; i < C; ++i) {
+        hi[i] = __uint_as_float(a[i]);
+        lo[i] = __uint_as_float(C == 8 ? b[i] : a[4 + i]);
+    }
+}
+template <int ROWS, int C>
+__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, int r0, const float (&hi)[C],
+                                             const float (&lo)[C]) {
+    uint32_t a[8], b[8];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        a[i] = __float_as_uint(hi[i]);
+        (C == 8 ? b[i] : a[4 + i]) = __float_as_uint(lo[i]);
+    }
+    tmem_st8(taddr + r0, a);
+    if constexpr (C == 8) tmem_st8(taddr + ROWS + r0, b);
+    tmem_st_wait();
 }
 
+// Whether the phase of `bar` with parity `parity` has completed; never waits
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 // Four values as two e4m3 terms each (byte i: value i), x = hi + lo / shift
 __device__ __forceinline__ void split_e4m3x4(float x0, float x1, float x2, float x3, float shift,
                                              uint32_t& hi, uint32_t& lo) {
@@ -238,19 +272,26 @@ __device__ __forceinline__ uint64_t mn_chunk_desc(uint32_t smem_addr, uint32_t k
     return uint64_t((smem_addr >> 4) & 0x3FFFu) | uint64_t(kgroup >> 4) << 16 |
            uint64_t(chunk >> 4) << 32 | uint64_t(1) << 46;
 }
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
 __device__ __forceinline__ float warp_max(float x) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void consumers_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+template <int THREADS>
 __device__ __forceinline__ bool consumers_any(bool x) {
     int r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(int(x))
+        : "r"(int(x)), "n"(THREADS)
         : "memory");
     return r != 0;
 }
@@ -292,17 +333,18 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                const Kv8DecodeParams p) {
     using C = Kv8Cfg<ROWS>;
     constexpr int SUB = PAIR ? ROWS / 2 : ROWS;
+    constexpr int RW = C::RW, CT = C::CONSUMERS, PRODUCER = C::CONSUMERS / 32;
     constexpr int CH = ROWS < 8 ? ROWS : 8;  // rows per accumulator load
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full_k = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* empty_k = full_k + C::ST;
-    uint64_t* full_v = empty_k + C::ST;
-    uint64_t* empty_v = full_v + C::ST;
-    uint64_t* full_s = empty_v + C::ST;
-    uint64_t* s_done = full_s + C::ST;
-    uint64_t* o_done = s_done + 2;
+    uint64_t* full_v = full_k + C::ST;
+    uint64_t* full_s = full_v + C::ST;   // scales
+    uint64_t* s_done = full_s + C::ST;   // S^T computed: its K stage is free
+    uint64_t* o_done = s_done + C::ST;   // O^T summed: its V stage, scales and P are free
+    uint64_t* p_ready = o_done + C::ST;  // [2] P written, S^T read
+    uint64_t* q_ready = p_ready + 2;     // a segment's q written
     int* misc = reinterpret_cast<int*>(smem + C::OFF_MISC);
     volatile int* abort_flag = misc;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
@@ -313,19 +355,12 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
 
     griddep_launch_dependents();
     if (tid == 0) {
-        for (int s = 0; s < C::ST; ++s) {
-            mbar_init(full_k + s, 1);
-            mbar_init(empty_k + s, 1);
-            mbar_init(full_v + s, 1);
-            mbar_init(empty_v + s, 1);
-            mbar_init(full_s + s, 1);
-        }
-        for (int i = 0; i < 4; ++i) mbar_init(s_done + i, 1);
+        for (int i = 0; i < C::N_BAR; ++i) mbar_init(full_k + i, 1);
         *abort_flag = 0;
         range[0] = 0;
         fence_mbar_init();
     }
-    if (warp == 4) {
+    if (warp == PRODUCER) {
         tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();  // at once: the SM's other CTAs cannot allocate before
     }
@@ -393,7 +428,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
     Kv8Walk<SUB> walk;
     walk.start(p, first_item[0], first_item[1], first_item[2], first_item[3], range[0]);
 
-    if (warp == 4) {
+    if (warp == PRODUCER) {
         // ------------------------------------------------------------ producer
         // A tile is one copy per page it touches (128 rows at most), one lane each, and the
         // scales of its eight groups of 16 keys (a scale block is 16 keys or more): lane
@@ -440,7 +475,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 }
                 const int s = c % C::ST;
                 const uint32_t ph = ((c / C::ST) & 1) ^ 1;
-                ok = mbar_wait_warp(empty_k + s, ph, abort_flag);
+                ok = mbar_wait_warp(s_done + s, ph, abort_flag);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(full_k + s, C::TILE);
                 __syncwarp();
@@ -448,7 +483,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     tma_load_2d(smem + C::OFF_K + s * C::TILE + lane * box * 128, &tm_k,
                                 full_k + s, x, z);
                 ++copies[0];
-                ok = mbar_wait_warp(empty_v + s, ph, abort_flag);
+                ok = mbar_wait_warp(o_done + s, ph, abort_flag);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(full_v + s, C::TILE);
                 __syncwarp();
@@ -456,19 +491,17 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     tma_load_2d(smem + C::OFF_V + s * C::TILE + lane * box * 128, &tm_v,
                                 full_v + s, x, z);
                 ++copies[1];
-                // V's stage being free, so is the stage of scales: all four consumer warps
-                // have read them before that tile's P V was issued
+                // V's stage being free, so is the stage of scales: every consumer warp has
+                // read them before that tile's P V was issued
                 float vref = vs;
 #pragma unroll
                 for (int off = 4; off > 0; off >>= 1)
                     vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, off));
-                const float rel = vref > 0.f ? vs / vref : 0.f;
                 if (lane < 16)
                     reinterpret_cast<float4*>(smem + C::OFF_SC)[s * 16 + lane] =
-                        make_float4(ks, fmaxf(__log2f(rel), -60.f), rel * 32.f, 0.f);
+                        make_float4(ks, __log2f(vs), vs, 0.f);
                 if (lane < 16 && grp == 0)
-                    reinterpret_cast<float*>(smem + C::OFF_VREF)[s * 2 + half] =
-                        vref * 0.03125f;
+                    reinterpret_cast<float*>(smem + C::OFF_VREF)[s * 2 + half] = vref;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full_s + s);
             }
@@ -487,25 +520,85 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                         }
                 }
         }
+    } else if (warp == PRODUCER + 1) {
+        // ------------------------------------------------------------ MMA issuer
+        // S^T of the next tile goes out as soon as its keys are here and the tile before
+        // the last has left the buffer; P V as soon as P and the values are.  (Issuing four
+        // MMAs takes a few hundred cycles, so no consumer does it.)
+        if (lane == 0) {
+            const uint32_t idesc_s = idesc_e4m3_f32(128, C::N, 0, 0);
+            const uint32_t idesc_o = idesc_e4m3_f32(128, C::N, 1, 1);
+            const uint64_t dk = sw128_desc(smem_u32(smem + C::OFF_K), 16, 1024);
+            const uint64_t dv = sw128_desc(smem_u32(smem + C::OFF_V), C::TILE, 1024);
+            const uint64_t dq = sw128_desc(smem_u32(smem + C::OFF_Q), 16, 1024);
+            // P: [N / 16 chunks][128 keys][16 columns]
+            const uint64_t dp = mn_chunk_desc(smem_u32(smem + C::OFF_P), 128, 2048);
+            int x = 0, y = 0;  // next tile of S^T, of P V
+            bool ok = true;
+            for (int segment = 0; walk.left > 0 && ok; walk.next(p), ++segment) {
+                const int first = y, end = y + walk.segment();
+                ok = mbar_wait(q_ready, segment & 1, abort_flag);
+                uint64_t since = globaltimer_ns();  // of the last issue, as the clock checks see it
+                int polls = 0, issued = x + y;
+                while (ok && y < end) {
+                    if (x < end && x < y + 2 && mbar_test(full_k + x % C::ST, (x / C::ST) & 1)) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_ss_f8(tmem + (x & 1) * C::N,
+                                       dk + (((x % C::ST) * C::TILE + kk * 32) >> 4),
+                                       dq + ((kk * 32) >> 4), idesc_s, kk > 0);
+                        umma_commit(s_done + x % C::ST);
+                        ++x;
+                    }
+                    if (y < x && mbar_test(p_ready + (y & 1), (y >> 1) & 1) &&
+                        mbar_test(full_v + y % C::ST, (y / C::ST) & 1)) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            umma_ss_f8(tmem + 2 * C::N,
+                                       dv + (((y % C::ST) * C::TILE + kk * 32 * 128) >> 4),
+                                       dp + (((y & 1) * (C::N * 128) + kk * 512) >> 4), idesc_o,
+                                       y > first || kk > 0);
+                        umma_commit(o_done + y % C::ST);
+                        ++y;
+                    }
+                    if ((++polls & 63) == 0) {
+                        const uint64_t now = globaltimer_ns();
+                        if (issued != x + y) {
+                            issued = x + y;
+                            since = now;
+                        }
+                        if (now - since > kWaitLimitNs) {
+                            raise_device_error(kDevWaitTimeout);
+                            *abort_flag = 1;
+                        }
+                        ok = *abort_flag == 0;
+                    }
+                }
+            }
+        }
     } else {
         // ------------------------------------------------------------ consumers
-        const uint32_t idesc_s = idesc_e4m3_f32(128, C::N, 0, 0);
-        const uint32_t idesc_o = idesc_e4m3_f32(128, C::N, 1, 1);
-        const uint64_t dk = sw128_desc(smem_u32(smem + C::OFF_K), 16, 1024);
-        const uint64_t dv = sw128_desc(smem_u32(smem + C::OFF_V), C::TILE, 1024);
-        const uint64_t dq = sw128_desc(smem_u32(smem + C::OFF_Q), 16, 1024);
-        // P: [N / 16 chunks][128 keys][16 columns], so a thread stores its key's columns whole
-        const uint64_t dp = mn_chunk_desc(smem_u32(smem + C::OFF_P), 128, 2048);
-        const uint32_t sp = smem_u32(smem + C::OFF_P) + tid * 16;
-        const uint32_t lane_base = uint32_t(warp * 32) << 16;  // this warp's TMEM lanes
-        const uint32_t t_s = tmem + lane_base, t_o = t_s + 2 * C::N;
+        const int wg = warp >> 2;            // this warpgroup's rows: [R0, R0 + RW)
+        const int R0 = wg * RW;
+        const int t128 = tid & 127;          // this thread's key of a tile, and its dimension
+        // P is [N / 16 chunks][128 keys][16 columns]: a thread stores its key's columns whole
+        const uint32_t sp = smem_u32(smem + C::OFF_P) + t128 * 16;
+        const uint32_t t_s = tmem + (uint32_t((warp & 3) * 32) << 16);  // this warp's lanes
+        const uint32_t t_o = t_s + 2 * C::N;
         const uint32_t sq = smem_u32(smem + C::OFF_Q);
         float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
         float2* rows = reinterpret_cast<float2*>(smem + C::OFF_ROW);
         int2* limits = reinterpret_cast<int2*>(smem + C::OFF_LIM);
         int* next_ref = reinterpret_cast<int*>(smem + C::OFF_TOP);
+        float4* vrun = reinterpret_cast<float4*>(smem + C::OFF_VRUN);  // vrun, log2, 1 / vrun
         float* so = reinterpret_cast<float*>(smem + C::OFF_P);  // [ROWS][128], P unused
-        const int my_half = PAIR ? tid >> 6 : 0;  // of this thread's dimension
+        const int my_half = PAIR ? t128 >> 6 : 0;  // of this thread's dimension
+        // the KV heads (of a pair) of this warpgroup's rows: half0 and, with NH = 2, half0 + 1
+        constexpr int NH = PAIR && C::WGS == 1 ? 2 : 1;
+        const int half0 = PAIR && C::WGS == 2 ? wg : 0;
+        auto half_of = [](int r) { return NH == 2 ? r / SUB : 0; };  // of row R0 + r
         int c = 0;
         bool aborted = false, first_segment = true;
         for (; walk.left > 0; walk.next(p), first_segment = false) {
@@ -514,7 +607,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             const bool whole = walk.off == 0 && segment == walk.n;
             // --- q rows of this item as two e4m3 terms; the MMAs that read the last
             // item's rows have completed
-            for (int r = warp; r < ROWS; r += 4) {
+            for (int r = warp; r < ROWS; r += CT / 32) {
                 int i, h;
                 const bool valid = kv8_row<ROWS, PAIR>(p, walk.seq, hg, walk.u, r, i, h);
                 constexpr int D = PAIR ? 64 : 128;
@@ -554,11 +647,12 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 }
             }
             fence_proxy_async();
-            consumers_sync();
+            consumers_sync<CT>();
+            if (tid == 0) mbar_arrive(q_ready);
 
-            float l[ROWS], o[ROWS];
+            float l[RW];
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) l[r] = 0.f, o[r] = 0.f;
+            for (int r = 0; r < RW; ++r) l[r] = 0.f;
             // keys that every row sees, in tiles between which no mask is needed
             const int t0 = walk.keys.first() + walk.off;
             const int last = walk.seq.len - walk.seq.n;  // position of query 0
@@ -566,101 +660,72 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             const int i_hi = min((walk.u * SUB + SUB - 1) / p.G, walk.seq.n - 1);
             const int all_hi = last + i_lo + 1;
             const int all_lo = p.window > 0 ? max(last + i_hi + 1 - p.window, 0) : 0;
-            // S^T of tile x (counted over the CTA) into its buffer
-            auto issue_s = [&](int x) {
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    umma_ss_f8(tmem + (x & 1) * C::N,
-                               dk + (((x % C::ST) * C::TILE + kk * 32) >> 4),
-                               dq + ((kk * 32) >> 4), idesc_s, kk > 0);
-                umma_commit(empty_k + x % C::ST);
-                umma_commit(s_done + (x & 1));
-            };
-            int s_next = c;          // thread 0: the first tile whose S^T is not issued
-            bool pending = false;    // the O^T of tile c - 1 is not in o yet
-            float vref_pending = 0.f;
-            const int c_end = c + segment;
-            auto issue_ahead = [&](int x) {  // tile x, if its keys are here
-                if (s_next == x && x < c_end && mbar_try_wait(full_k + x % C::ST, (x / C::ST) & 1)) {
-                    issue_s(x);
-                    ++s_next;
-                }
-            };
-            // adds the pending O^T
-            auto take_o = [&](int x) {
-                mbar_wait_warp(o_done + (x & 1), (x >> 1) & 1, abort_flag);
-                tc_fence_after();
-#pragma unroll
-                for (int r0 = 0; r0 < ROWS; r0 += CH) {
-                    float f[CH];
-                    tmem_ld_rows<ROWS, CH>(t_o + (x & 1) * C::N, r0, 0.03125f, f);
-#pragma unroll
-                    for (int j = 0; j < CH; ++j) o[r0 + j] = fmaf(f[j], vref_pending, o[r0 + j]);
-                }
-                tc_fence_before();
-                pending = false;
+            auto wait_o = [&](int x) {  // P V of tile x (counted over the CTA) has completed
+                return mbar_wait_warp(o_done + x % C::ST, (x / C::ST) & 1, abort_flag);
             };
             for (int t = t0; t < t0 + segment; ++t, ++c) {
                 const int s = c % C::ST;
                 const uint32_t ph = (c / C::ST) & 1;
                 bool ok = true;
-                if (tid == 0 && s_next == c) {
-                    ok = mbar_wait(full_k + s, ph, abort_flag);
-                    if (ok) issue_s(c);
-                    ++s_next;
-                }
-                __syncwarp();
-                const int key = t * 128 + tid;
+                const int key = t * 128 + t128;
                 ok &= mbar_wait_warp(full_s + s, ph, abort_flag);
-                float4 sc[2];
-                sc[0] = reinterpret_cast<float4*>(smem + C::OFF_SC)[s * 16 + (tid >> 4)];
-                if constexpr (PAIR)
-                    sc[1] = reinterpret_cast<float4*>(smem + C::OFF_SC)[s * 16 + 8 + (tid >> 4)];
-                const float vref =
-                    reinterpret_cast<float*>(smem + C::OFF_VREF)[s * 2 + my_half];
-                ok &= mbar_wait_warp(s_done + (c & 1), (c >> 1) & 1, abort_flag);
+                float4 sc[NH];   // K scale, log2 of the V scale, V scale
+                float vref[NH];  // the tile's largest V scale
+#pragma unroll
+                for (int j = 0; j < NH; ++j) {
+                    sc[j] = reinterpret_cast<float4*>(
+                        smem + C::OFF_SC)[s * 16 + (half0 + j) * 8 + (t128 >> 4)];
+                    vref[j] = reinterpret_cast<float*>(smem + C::OFF_VREF)[s * 2 + half0 + j];
+                }
+                // P's buffer is free once the tile before the last has used it
+                if (c >= 2) ok &= wait_o(c - 2);
+                ok &= mbar_wait_warp(s_done + s, ph, abort_flag);
                 tc_fence_after();
-                if (tid == 0) issue_ahead(c + 1);
-                __syncwarp();
                 const bool edge = t * 128 < all_lo || t * 128 + 128 > all_hi;
                 const uint32_t t_sc = t_s + (c & 1) * C::N;
                 const uint32_t sp_c = sp + (c & 1) * (C::N * 128);
-                // logits of rows r0 .. r0 + CH - 1 in log2 units, -inf where not seen
+                // logits of rows R0 + r0 .. in log2 units, -inf where not seen
                 auto logits = [&](int r0, float (&f)[CH]) {
-                    tmem_ld_rows<ROWS, CH>(t_sc, r0, 0.0625f, f);
+                    float lo[CH];
+                    tmem_ld_rows<ROWS, CH>(t_sc, R0 + r0, f, lo);
 #pragma unroll
                     for (int j = 0; j < CH; ++j)
-                        f[j] *= sc[PAIR ? (r0 + j) / SUB : 0].x * rows[r0 + j].x;
+                        f[j] = fmaf(lo[j], 0.0625f, f[j]) *
+                               (sc[half_of(r0 + j)].x * rows[R0 + r0 + j].x);
                     if (edge) {
 #pragma unroll
                         for (int j = 0; j < CH; ++j) {
-                            const int2 lim = limits[r0 + j];
+                            const int2 lim = limits[R0 + r0 + j];
                             if (key < lim.x || key >= lim.y) f[j] = -INFINITY;
                         }
                     }
                 };
                 // V rows that no query sees may hold any code: a weight of 0 times NaN
                 // would still reach O
-                if (t * 128 < walk.keys.lo || t * 128 + 128 > walk.keys.hi) {
+                if (wg == 0 && (t * 128 < walk.keys.lo || t * 128 + 128 > walk.keys.hi)) {
                     ok &= mbar_wait_warp(full_v + s, ph, abort_flag);
                     if (key < walk.keys.lo || key >= walk.keys.hi) {
-                        const uint32_t v = smem_u32(smem + C::OFF_V + s * C::TILE) + tid * 128;
+                        const uint32_t v = smem_u32(smem + C::OFF_V + s * C::TILE) + t128 * 128;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) st_shared_v4(v + j * 16, 0u, 0u, 0u, 0u);
                     }
                 }
                 // the weights relative to the rows' references: their terms u, and P
-                float u[ROWS];
+                float u[RW];
                 for (int pass = 0;; ++pass) {
                     bool high = pass == 0;
                     if (pass > 0 || t > t0) {
-                        uint32_t codes[C::N / 4];  // hi of every row, then lo
-                        float above[2] = {-INFINITY, -INFINITY};
+                        uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+                        float above[NH], d[NH], g[NH];
 #pragma unroll
-                        for (int i = 0; i < C::N / 4; ++i) codes[i] = 0u;
+                        for (int j = 0; j < NH; ++j) {
+                            const float4 v = vrun[half0 + j];
+                            above[j] = -INFINITY;
+                            d[j] = fmaxf(sc[j].y - v.y, -60.f);
+                            g[j] = sc[j].z * v.z * 32.f;
+                        }
 #pragma unroll
-                        for (int r0 = 0; r0 < ROWS; r0 += CH) {
+                        for (int r0 = 0; r0 < RW; r0 += CH) {
                             float f[CH];
                             logits(r0, f);
 #pragma unroll
@@ -668,114 +733,146 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                                 float w[4];
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
-                                    const int r = r0 + j + e, half = PAIR ? r / SUB : 0;
-                                    const float x = f[j + e] - rows[r].y;
+                                    const int r = r0 + j + e, half = half_of(r);
+                                    const float x = f[j + e] - rows[R0 + r].y;
                                     above[half] = fmaxf(above[half], x);
                                     u[r] = ex2_approx(x);
-                                    w[e] = u[r] * sc[half].z;
+                                    w[e] = u[r] * g[half];
                                 }
-                                split_e4m3x4(w[0], w[1], w[2], w[3], 32.f, codes[(r0 + j) / 4],
-                                             codes[(ROWS + r0 + j) / 4]);
+                                split_e4m3x4(w[0], w[1], w[2], w[3], 32.f, hi[(r0 + j) / 4],
+                                             lo[(r0 + j) / 4]);
                             }
                         }
-#pragma unroll
-                        for (int i = 0; i < C::N / 16; ++i)
-                            st_shared_v4(sp_c + i * 2048, codes[4 * i], codes[4 * i + 1],
-                                         codes[4 * i + 2], codes[4 * i + 3]);
+                        // columns: hi of every row, then lo
+                        if constexpr (RW == 4) {
+                            st_shared_v4(sp_c, hi[0], lo[0], 0u, 0u);
+                        } else if constexpr (ROWS == 8) {
+                            st_shared_v4(sp_c, hi[0], hi[1], lo[0], lo[1]);
+                        } else if constexpr (RW == 8) {
+                            st_shared_v2(sp_c + R0, hi[0], hi[1]);
+                            st_shared_v2(sp_c + 2048 + R0, lo[0], lo[1]);
+                        } else {
+                            st_shared_v4(sp_c + wg * 2048, hi[0], hi[1], hi[2], hi[3]);
+                            st_shared_v4(sp_c + (2 + wg) * 2048, lo[0], lo[1], lo[2], lo[3]);
+                        }
                         // (the second pass has its tile's own references)
-                        high = pass == 0 && (above[0] + sc[0].y > 3.f ||
-                                             (PAIR && above[1] + sc[PAIR ? 1 : 0].y > 3.f));
+                        high = pass == 0 &&
+                               (above[0] + d[0] > 3.f || above[NH - 1] + d[NH - 1] > 3.f);
                     }
                     if (__any_sync(0xffffffffu, high)) {
+                        float d[NH];  // relative to what vrun becomes
+#pragma unroll
+                        for (int j = 0; j < NH; ++j)
+                            d[j] = fmaxf(
+                                sc[j].y - __log2f(t == t0 ? vref[j]
+                                                          : fmaxf(vref[j], vrun[half0 + j].x)),
+                                -60.f);
                         float top = -INFINITY;  // lane r: the warp's largest z + d of row r
 #pragma unroll
-                        for (int r0 = 0; r0 < ROWS; r0 += CH) {
+                        for (int r0 = 0; r0 < RW; r0 += CH) {
                             float f[CH];
                             logits(r0, f);
 #pragma unroll
                             for (int j = 0; j < CH; ++j) {
-                                const int r = r0 + j;
-                                const float mx = warp_max(f[j] + sc[PAIR ? r / SUB : 0].y);
-                                if (lane == r) top = mx;
+                                const float mx = warp_max(f[j] + d[half_of(r0 + j)]);
+                                if (lane == r0 + j) top = mx;
                             }
                         }
-                        if (lane < ROWS) atomicMax(next_ref + lane, ordered(top));
+                        if (lane < RW) atomicMax(next_ref + R0 + lane, ordered(top));
                     }
                     fence_proxy_async();
                     tc_fence_before();
-                    if (!consumers_any(high || !ok)) break;
-                    aborted = consumers_any(!ok);
+                    if (!consumers_any<CT>(high || !ok)) break;
+                    if (t > t0) ok &= wait_o(c - 1);
+                    aborted = consumers_any<CT>(!ok);
                     if (aborted) break;
-                    if (pending) take_o(c - 1);
+                    tc_fence_after();
+                    float v[NH], ratio[NH];
 #pragma unroll
-                    for (int r = 0; r < ROWS; ++r) {
-                        const float alpha = ex2_approx(rows[r].y - unordered(next_ref[r]));
-                        l[r] *= alpha;
-                        o[r] *= alpha;
+                    for (int j = 0; j < NH; ++j) {
+                        const float v0 = t > t0 ? vrun[half0 + j].x : 0.f;
+                        v[j] = fmaxf(vref[j], v0);
+                        ratio[j] = v[j] > 0.f ? v0 / v[j] : 0.f;
                     }
-                    consumers_sync();
+#pragma unroll
+                    for (int r0 = 0; r0 < RW; r0 += CH) {
+                        float alpha[CH];
+#pragma unroll
+                        for (int j = 0; j < CH; ++j) {
+                            const int r = r0 + j;
+                            alpha[j] = ex2_approx(rows[R0 + r].y - unordered(next_ref[R0 + r]));
+                            l[r] *= alpha[j];
+                            alpha[j] *= ratio[half_of(r)];
+                        }
+                        if (t > t0) {
+                            float hi[CH], lo[CH];
+                            tmem_ld_rows<ROWS, CH>(t_o, R0 + r0, hi, lo);
+#pragma unroll
+                            for (int j = 0; j < CH; ++j) hi[j] *= alpha[j], lo[j] *= alpha[j];
+                            tmem_st_rows<ROWS, CH>(t_o, R0 + r0, hi, lo);
+                        }
+                    }
+                    tc_fence_before();
+                    consumers_sync<CT>();
                     if (tid < ROWS) rows[tid].y = unordered(next_ref[tid]);
-                    consumers_sync();
+                    if (t128 < NH && (PAIR || wg == 0)) {
+                        const float x = t128 ? v[NH - 1] : v[0];
+                        vrun[half0 + t128] =
+                            make_float4(x, __log2f(x), x > 0.f ? 1.f / x : 0.f, 0.f);
+                    }
+                    consumers_sync<CT>();
                 }
                 if (aborted) break;
-                if (tid == 0) {
-                    if (mbar_wait(full_v + s, ph, abort_flag)) {
-                        tc_fence_after();
+                if (tid == 0) mbar_arrive(p_ready + (c & 1));
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_ss_f8(tmem + (2 + (c & 1)) * C::N,
-                                       dv + ((s * C::TILE + kk * 32 * 128) >> 4),
-                                       dp + (((c & 1) * (C::N * 128) + kk * 512) >> 4), idesc_o,
-                                       kk > 0);
-                        umma_commit(empty_v + s);
-                        umma_commit(o_done + (c & 1));
-                    }
-                    issue_ahead(c + 1);
-                }
-                __syncwarp();
-#pragma unroll
-                for (int r = 0; r < ROWS; ++r) l[r] += u[r];
-                // (a wait that runs out here shows in the next tile's, or below)
-                if (pending) take_o(c - 1);
-                pending = true;
-                vref_pending = vref;
+                for (int r = 0; r < RW; ++r) l[r] += u[r];
             }
-            if (pending) take_o(c - 1);
             // --- end of the segment: sums over the keys, then the rows' results
-            aborted = consumers_any(aborted || *abort_flag != 0);
+            if (!aborted) wait_o(c - 1);
+            tc_fence_after();
+            aborted = consumers_any<CT>(aborted || *abort_flag != 0);
+            const float unit = vrun[my_half].x * 0.03125f;
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) {
+            for (int r0 = 0; r0 < RW; r0 += CH) {
+                float hi[CH], lo[CH];
+                tmem_ld_rows<ROWS, CH>(t_o, R0 + r0, hi, lo);
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1)
-                    l[r] += __shfl_xor_sync(0xffffffffu, l[r], off);
-                if (lane == 0) red[warp * ROWS + r] = l[r];
-                so[r * 128 + tid] = o[r];  // (read back by this thread)
+                for (int j = 0; j < CH; ++j) {  // (so is read back by this thread)
+                    so[(R0 + r0 + j) * 128 + t128] = fmaf(lo[j], 0.03125f, hi[j]) * unit;
+                    float x = l[r0 + j];
+#pragma unroll
+                    for (int off = 16; off > 0; off >>= 1)
+                        x += __shfl_xor_sync(0xffffffffu, x, off);
+                    if (lane == 0) red[(R0 + r0 + j) * 4 + (warp & 3)] = x;
+                }
             }
-            consumers_sync();
+            tc_fence_before();
+            consumers_sync<CT>();
             const long long item = ((long long)walk.b * p.groups + hg) * p.units + walk.u;
             const size_t part = size_t(blockIdx.x) * 2 + (first_segment ? 0 : 1);
 #pragma unroll 1
-            for (int r = 0; r < ROWS; ++r) {
-                float sum = (red[r] + red[ROWS + r]) + (red[2 * ROWS + r] + red[3 * ROWS + r]);
-                float acc = so[r * 128 + tid];
+            for (int r = R0; r < R0 + RW; ++r) {
+                const float4 x = reinterpret_cast<float4*>(red)[r];
+                float sum = (x.x + x.y) + (x.z + x.w);
+                float acc = so[r * 128 + t128];
                 // a wait gave up (device error word set): an empty result, so that no stale
                 // memory is picked up
                 if (aborted) sum = 0.f, acc = 0.f;
                 if (!whole) {
-                    p.part_o[(part * ROWS + r) * 128 + tid] = acc;
-                    if (tid == 0) p.part_ml[part * ROWS + r] = make_float2(rows[r].y, sum);
+                    p.part_o[(part * ROWS + r) * 128 + t128] = acc;
+                    if (t128 == 0) p.part_ml[part * ROWS + r] = make_float2(rows[r].y, sum);
                 } else {
-                    kv8_store<ROWS, PAIR>(p, walk.seq, walk.b, hg, walk.u, r, tid, acc, sum,
+                    kv8_store<ROWS, PAIR>(p, walk.seq, walk.b, hg, walk.u, r, t128, acc, sum,
                                           rows[r].y);
                 }
             }
             if (tid == 0 && walk.off == 0) p.meta[item] = range[1] + (range[0] - walk.left);
-            consumers_sync();  // red, rows and P are free again
+            consumers_sync<CT>();  // red, rows and P are free again
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == PRODUCER) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }

@@ -517,7 +517,7 @@ int gqa_attn_kv8_gather(const void* k8, const void* v8, const float* k_scale,
  *     (a range that does not fit raises device error 2 and is left out).
  *   block_table [B, max_pages], seqlens_k [B]: as gqa_attn_decode_paged; only entries of
  *     pages that hold a visible key are read.
- * Scales: any finite positive fp32.  What lies in the pool outside the visible keys is
+ * Scales: any finite normal positive fp32.  What lies in the pool outside the visible keys is
  * never used, whatever its codes.  workspace: gqa_attn_kv8_decode_workspace_bytes(B, Sq, Hq,
  * Hkv, D) bytes, 16-byte aligned, private to the call until it has run: a parameter and
  * not the registered workspace, so that calls on several streams and in several captured
