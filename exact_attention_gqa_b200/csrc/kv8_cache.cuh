@@ -58,6 +58,8 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables(const KvTablesParams
     __shared__ long long warp_sum[3][kTablesThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ps = 1 << p.page_shift;
+    griddep_launch_dependents();
+    griddep_wait();
     const long long cap = (long long)p.max_pages << p.page_shift;
     const int per = (p.B + kTablesThreads - 1) / kTablesThreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
@@ -215,6 +217,8 @@ __global__ void __launch_bounds__(256) kv8_append(const Kv8AppendParams p) {
     const int lane = threadIdx.x & 31;
     const long long job = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int t = int(job / p.Hkv), h = int(job - (long long)t * p.Hkv);
+    griddep_launch_dependents();
+    griddep_wait();
     if (t >= p.T) return;
     const int slot = __ldg(p.slot_map + t);
     if (slot < 0 || slot >= p.slots) {
@@ -307,6 +311,8 @@ constexpr int kGatherRows = 16;
 __global__ void __launch_bounds__(256) kv8_gather(const Kv8GatherParams p) {
     __shared__ int src[kGatherRows];  // row of the pool, -1: none
     const int row0 = blockIdx.x * kGatherRows;
+    griddep_launch_dependents();
+    griddep_wait();
     if (threadIdx.x < kGatherRows) {
         const int t = row0 + threadIdx.x;
         int s = -1;

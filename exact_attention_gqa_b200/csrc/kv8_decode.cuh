@@ -53,7 +53,7 @@ struct Kv8DecodeParams {
     const int* cu_seqlens_q;  // [B + 1] or null: Sq queries each
     float* part_o;            // [CTAs, 2, R, 128] fp32 partials of a CTA's cut items
     float2* part_ml;          // [CTAs, 2, R] reference (log2 units) and sum
-    long long* meta;          // [items]: an item's first tile of its head group's; then: all of them
+    int2* meta;               // [items] parts of an item; 2 x first team + (its second partial)
     int B, Sq, total_q, Hq, Hkv, G;
     int groups, units;        // head groups (KV heads, or pairs of them); row units of each
     int width, teams;         // CTAs of a team (divides groups), teams of the grid
@@ -182,8 +182,11 @@ struct Kv8Walk {
 __device__ __forceinline__ int kv8_teams(long long tiles, int teams) {
     return int(min(tiles, (long long)teams));
 }
+__device__ __forceinline__ long long kv8_div(long long x, long long y) {  // x >= 0, y > 0
+    return ((x | y) >> 32) == 0 ? (long long)(uint32_t(x) / uint32_t(y)) : x / y;
+}
 __device__ __forceinline__ long long kv8_range_start(long long tiles, int team, int teams) {
-    return tiles * team / teams;
+    return kv8_div(tiles * team, teams);
 }
 // float bits as an int that orders like the float, and back
 __device__ __forceinline__ int ordered(float x) {
@@ -349,11 +352,10 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
     volatile int* abort_flag = misc;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
     volatile int* first_item = misc + 2;                                   // b, hs, u, off
-    volatile long long* range = reinterpret_cast<volatile long long*>(misc + 6);  // left, first tile
+    volatile long long* range = reinterpret_cast<volatile long long*>(misc + 6);  // left, first tile; all tiles
     long long* scan = reinterpret_cast<long long*>(smem + C::OFF_P);       // before P is used
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    griddep_launch_dependents();
     if (tid == 0) {
         for (int i = 0; i < C::N_BAR; ++i) mbar_init(full_k + i, 1);
         *abort_flag = 0;
@@ -363,7 +365,13 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
     if (warp == PRODUCER) {
         tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();  // at once: the SM's other CTAs cannot allocate before
+        if (lane == 0) {
+            tma_prefetch_desc(&tm_k);
+            tma_prefetch_desc(&tm_v);
+        }
     }
+    griddep_launch_dependents();
+    griddep_wait();  // whatever wrote the cache, the tables and q has completed
 
     // Every CTA adds up the tiles of one head group and finds the item its range starts in.
     const int team = blockIdx.x / p.width, member = blockIdx.x - team * p.width;
@@ -396,7 +404,6 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         const bool works = team < teams;
         const long long lo = works ? kv8_range_start(all, team, teams) : 0;
         const long long hi = works ? kv8_range_start(all, team + 1, teams) : 0;
-        if (blockIdx.x == 0 && tid == 0) p.meta[(long long)p.B * p.groups * p.units] = all;
         if (lo < hi && lo >= before && lo < before + mine) {
             long long at = lo - before;
             int b = b0;
@@ -405,7 +412,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 at -= t * sets;
                 t = tiles_of(++b);
             }
-            const int hs = int(at / t);
+            const int hs = sets > 1 ? int(at / t) : 0;
             at -= hs * t;
             const Kv8Seq s = kv8_seq(p, b);
             int u = 0, n = kv8_keys<SUB>(p, s, 0).tiles();
@@ -419,6 +426,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             first_item[3] = int(at);
             range[0] = hi - lo;
             range[1] = lo;
+            range[2] = all;
         }
     }
     tc_fence_before();
@@ -434,10 +442,6 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         // scales of its eight groups of 16 keys (a scale block is 16 keys or more): lane
         // 8 * half + group fetches those of its group.  Their loads are under way while the
         // lanes wait for free stages.
-        if (lane == 0) {
-            tma_prefetch_desc(&tm_k);
-            tma_prefetch_desc(&tm_v);
-        }
         const int box = min(1 << p.page_shift, 128), boxes = 128 / box;
         const int half = (lane >> 3) & 1, grp = lane & 7;
         int c = 0, copies[2] = {0, 0};  // tiles; copies of K and of V issued
@@ -866,7 +870,15 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                                           rows[r].y);
                 }
             }
-            if (tid == 0 && walk.off == 0) p.meta[item] = range[1] + (range[0] - walk.left);
+            if (tid == 0 && walk.off == 0) {
+                int parts = 1;
+                if (!whole) {  // the team with the item's last tile is where it ends
+                    const long long end = range[1] + (range[0] - walk.left) + walk.n;
+                    const int teams = kv8_teams(range[2], p.teams);
+                    parts = int(kv8_div(end * teams - 1, range[2])) - team + 1;
+                }
+                p.meta[item] = make_int2(parts, 2 * team + (first_segment ? 0 : 1));
+            }
             consumers_sync<CT>();  // red, rows and P are free again
         }
     }
@@ -881,56 +893,70 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
 // One CTA per (row, item): joins the partials of an item that several teams shared, and
 // writes the rows that no key reached.  With reference M = max_s m_s (log2 units):
 // sum = sum_s 2^(m_s - M) sum_s, O = sum_s 2^(m_s - M) O_s / sum, L = ln 2 (M + log2 sum).
+// A warp takes every eighth partial, four at a time, with an online rescaling of its own.
+constexpr int kCombineWarps = 8;
 template <int ROWS, bool PAIR>
-__global__ void __launch_bounds__(128) kv8_combine(const Kv8DecodeParams p) {
+__global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine(const Kv8DecodeParams p) {
     constexpr int SUB = PAIR ? ROWS / 2 : ROWS;
-    __shared__ float factor[480];  // of each partial (at most one a CTA)
-    __shared__ float red[2][4];
+    __shared__ __align__(16) float so[kCombineWarps][128];
+    __shared__ float2 sml[kCombineWarps];
     const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const long long item = blockIdx.y + (long long)blockIdx.z * 65535;
-    const long long items = (long long)p.B * p.groups * p.units;
-    if (item >= items) return;
-    const int u = int(item % p.units);
-    const int hg = int(item / p.units % p.groups);
-    const int b = int(item / p.units / p.groups);
+    const uint32_t item = blockIdx.y + blockIdx.z * 65535u;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (item >= uint32_t(p.B) * p.groups * p.units) return;
+    const int2 meta = p.meta[item];  // (undefined for an item without tiles)
+    const uint32_t bh = item / uint32_t(p.units);
+    const int u = int(item - bh * p.units), b = int(bh / uint32_t(p.groups));
+    const int hg = int(bh - uint32_t(b) * p.groups);
     const Kv8Seq seq = kv8_seq(p, b);
     int i, h;
     if (!kv8_row<ROWS, PAIR>(p, seq, hg, u, r, i, h)) return;
-    const int n = kv8_keys<SUB>(p, seq, u).tiles();
-    griddep_wait();
-    float M = kNoKey, sum = 0.f, acc = 0.f;
-    if (n > 0) {
-        const long long all = p.meta[items], first = p.meta[item];
-        const int teams = kv8_teams(all, p.teams);
-        const int c0 = int(((first + 1) * teams - 1) / all);
-        const int c1 = int(((first + n) * teams - 1) / all);
-        if (c0 == c1) return;  // one CTA has written it
-        // the first team's share is its second partial unless its range starts there
-        const bool cut = kv8_range_start(all, c0, teams) != first;
-        const int member = hg % p.width, parts = c1 - c0 + 1;
-        auto part = [&](int x) {  // partial x of the item, its row r
-            return (size_t((c0 + x) * p.width + member) * 2 + (x == 0 && cut ? 1 : 0)) * ROWS + r;
-        };
-        for (int x = tid; x < parts; x += 128) M = fmaxf(M, p.part_ml[part(x)].x);
-        M = warp_max(M);
-        if (lane == 0) red[0][warp] = M;
-        __syncthreads();
-        M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-        for (int x = tid; x < parts; x += 128) {
-            const float2 ml = p.part_ml[part(x)];
-            const float f = exp2f(ml.x - M);
-            factor[x] = f;
-            sum += f * ml.y;
+    const int parts = kv8_keys<SUB>(p, seq, u).tiles() > 0 ? meta.x : 0;
+    if (parts == 1) return;  // one CTA has written it
+    float m = kNoKey, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    const int team = meta.y >> 1, member = hg % p.width;
+    for (int x0 = warp; x0 < parts; x0 += 4 * kCombineWarps) {
+        float2 ml[4];
+        float4 o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int x = x0 + j * kCombineWarps;
+            ml[j] = make_float2(kNoKey, 0.f);
+            o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (x < parts) {
+                const size_t at = (size_t((team + x) * p.width + member) * 2 +
+                                   (x == 0 ? meta.y & 1 : 0)) * ROWS + r;
+                ml[j] = p.part_ml[at];
+                o[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
+            }
         }
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) red[1][warp] = sum;
-        __syncthreads();
-        sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-#pragma unroll 8
-        for (int x = 0; x < parts; ++x) acc += factor[x] * p.part_o[part(x) * 128 + tid];
+        for (int j = 0; j < 4; ++j) {
+            const float m1 = fmaxf(m, ml[j].x);
+            const float a = ex2_approx(m - m1), f = ex2_approx(ml[j].x - m1);
+            m = m1;
+            sum = sum * a + f * ml[j].y;
+            acc[0] = acc[0] * a + f * o[j].x;
+            acc[1] = acc[1] * a + f * o[j].y;
+            acc[2] = acc[2] * a + f * o[j].z;
+            acc[3] = acc[3] * a + f * o[j].w;
+        }
     }
-    kv8_store<ROWS, PAIR>(p, seq, b, hg, u, r, tid, acc, sum, M);
+    reinterpret_cast<float4*>(so[warp])[lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (lane == 0) sml[warp] = make_float2(m, sum);
+    __syncthreads();
+    if (tid >= 128) return;
+    float M = kNoKey, total = 0.f, out = 0.f;
+#pragma unroll
+    for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, sml[w].x);
+#pragma unroll
+    for (int w = 0; w < kCombineWarps; ++w) {
+        const float f = ex2_approx(sml[w].x - M);
+        total += f * sml[w].y;
+        out += f * so[w][tid];
+    }
+    kv8_store<ROWS, PAIR>(p, seq, b, hg, u, r, tid, out, total, M);
 }
 
 }  // namespace gqa

@@ -36,6 +36,24 @@ bool make_map_kv8(CUtensorMap* m, const void* base, long long rows, int width, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A launch that may begin while the kernel before it in the stream ends: every kernel of
+// this file waits for that one (griddep_wait) before it touches global memory.
+template <typename... Params, typename... Args>
+int launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
+               const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
 // How a kv8 decode's query rows are cut: `rows` per pass (both heads' of a pair at D = 64),
 // as few as hold all G * Sq rows of a KV head, 32 at most; then several units.
 constexpr int kKv8MaxCtas = 480;
@@ -54,7 +72,7 @@ Kv8Plan kv8_plan(int B, int Sq, int Hq, int Hkv, int D) {
     pl.units = int((sub * heads + pl.rows - 1) / pl.rows);
     pl.items = (long long)B * pl.groups * pl.units;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    pl.off_ml = up(size_t(pl.items + 1) * 8);
+    pl.off_ml = up(size_t(pl.items) * 8);
     pl.off_o = pl.off_ml + up(size_t(kKv8MaxCtas) * 2 * pl.rows * 8);
     pl.bytes = pl.off_o + size_t(kKv8MaxCtas) * 2 * pl.rows * 128 * 4;
     return pl;
@@ -111,8 +129,7 @@ int gqa_attn_kv_tables(const int* cached_lens, const int* new_lens, const int* f
     if (rc != GQA_OK) return rc;
     const int want = (max_tokens + gqa::kTablesThreads - 1) / gqa::kTablesThreads;
     const int grid = std::max(1, std::min(want, dev->sms));
-    gqa::kv_tables<<<grid, gqa::kTablesThreads, smem, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+    return launch_pdl(gqa::kv_tables, dim3(grid), gqa::kTablesThreads, smem, stream, p);
 }
 
 int gqa_attn_kv8_append(const void* k, const void* v, const int* slot_map, void* k8, void* v8,
@@ -144,11 +161,7 @@ int gqa_attn_kv8_append(const void* k, const void* v, const int* slot_map, void*
     p.sb_shift = log2_exact(scale_block);
     p.slots = num_pages * page_size;
     const dim3 g(static_cast<unsigned>(grid), 2);
-    if (D == 128)
-        gqa::kv8_append<128><<<g, 256, 0, stream>>>(p);
-    else
-        gqa::kv8_append<64><<<g, 256, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+    return launch_pdl(D == 128 ? gqa::kv8_append<128> : gqa::kv8_append<64>, g, 256, 0, stream, p);
 }
 
 int gqa_attn_kv8_gather(const void* k8, const void* v8, const float* k_scale,
@@ -183,8 +196,7 @@ int gqa_attn_kv8_gather(const void* k8, const void* v8, const float* k_scale,
     p.sb_shift = log2_exact(scale_block);
     p.max_pages = max_pages;
     const dim3 g((total + gqa::kGatherRows - 1) / gqa::kGatherRows, 2);
-    gqa::kv8_gather<<<g, 256, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+    return launch_pdl(gqa::kv8_gather, g, 256, 0, stream, p);
 }
 
 size_t gqa_attn_kv8_decode_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D) {
@@ -230,7 +242,7 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
     p.seqlens_k = seqlens_k;
     p.cu_seqlens_q = cu_seqlens_q;
     char* ws = static_cast<char*>(workspace);
-    p.meta = reinterpret_cast<long long*>(ws);
+    p.meta = reinterpret_cast<int2*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
     p.part_o = reinterpret_cast<float*>(ws + pl.off_o);
     p.B = B;
@@ -266,21 +278,13 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
         p.teams = int(std::min<long long>(
             tiles, std::min(C::CTAS_PER_SM * sms, kKv8MaxCtas) / p.width));
         const int grid = p.teams * p.width;
-        gqa::kv8_decode<rows(), pair()><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(tk, tv, p);
-        if (cudaGetLastError() != cudaSuccess) return GQA_ERR_CUDA;
-        cudaLaunchConfig_t cfg = {};
-        const unsigned y = unsigned(std::min<long long>(pl.items, 65535));
-        cfg.gridDim = dim3(rows(), y, unsigned((pl.items + 65534) / 65535));
-        cfg.blockDim = dim3(128);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, gqa::kv8_combine<rows(), pair()>, p) == cudaSuccess
-                   ? GQA_OK
-                   : GQA_ERR_CUDA;
+        const int r2 = launch_pdl(gqa::kv8_decode<rows(), pair()>, dim3(grid), C::THREADS,
+                                  C::SMEM_BYTES, stream, tk, tv, p);
+        if (r2 != GQA_OK) return r2;
+        const dim3 g(rows(), unsigned(std::min<long long>(pl.items, 65535)),
+                     unsigned((pl.items + 65534) / 65535));
+        return launch_pdl(gqa::kv8_combine<rows(), pair()>, g, 32 * gqa::kCombineWarps, 0, stream,
+                          p);
     };
     auto pick = [&](auto pair, int bit) {
         using std::integral_constant;
