@@ -217,7 +217,6 @@ __global__ void __launch_bounds__(256) kv8_append(const Kv8AppendParams p) {
     const int lane = threadIdx.x & 31;
     const long long job = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int t = int(job / p.Hkv), h = int(job - (long long)t * p.Hkv);
-    griddep_launch_dependents();
     griddep_wait();
     if (t >= p.T) return;
     const int slot = __ldg(p.slot_map + t);
@@ -311,7 +310,6 @@ constexpr int kGatherRows = 16;
 __global__ void __launch_bounds__(256) kv8_gather(const Kv8GatherParams p) {
     __shared__ int src[kGatherRows];  // row of the pool, -1: none
     const int row0 = blockIdx.x * kGatherRows;
-    griddep_launch_dependents();
     griddep_wait();
     if (threadIdx.x < kGatherRows) {
         const int t = row0 + threadIdx.x;

@@ -53,7 +53,7 @@ struct Kv8DecodeParams {
     const int* cu_seqlens_q;  // [B + 1] or null: Sq queries each
     float* part_o;            // [CTAs, 2, R, 128] fp32 partials of a CTA's cut items
     float2* part_ml;          // [CTAs, 2, R] reference (log2 units) and sum
-    int2* meta;               // [items] parts of an item; 2 x first team + (its second partial)
+    int4* cut;                // [CTAs] the item that starts in a CTA's range and ends in another's
     int B, Sq, total_q, Hq, Hkv, G;
     int groups, units;        // head groups (KV heads, or pairs of them); row units of each
     int width, teams;         // CTAs of a team (divides groups), teams of the grid
@@ -67,22 +67,24 @@ struct Kv8Cfg {
     static constexpr int WGS = ROWS >= 16 ? 2 : 1;      // consumer warpgroups, rows split
     static constexpr int RW = ROWS / WGS;               // rows of each
     static constexpr int CTAS_PER_SM = 2;
-    static constexpr int ST = ROWS <= 16 ? 3 : 2;       // stages: what fits shared memory
+    static constexpr int STK = ROWS <= 16 ? 3 : 2;      // stages of K, and of V and scales:
+    static constexpr int STV = STK;                     // what fits shared memory
     static constexpr int TILE = 128 * 128;              // bytes of K or V per stage
     static constexpr int N = ROWS <= 8 ? 16 : 2 * ROWS;  // MMA columns: hi and lo of each row
     static constexpr int OFF_K = 0;
-    static constexpr int OFF_V = ST * TILE;
-    static constexpr int OFF_Q = 2 * ST * TILE;
+    static constexpr int OFF_V = STK * TILE;
+    static constexpr int OFF_Q = OFF_V + STV * TILE;
     static constexpr int OFF_P = OFF_Q + N * 128;       // two buffers
-    static constexpr int OFF_SC = OFF_P + 2 * N * 128;  // [ST][2 halves][8 groups] float4
-    static constexpr int OFF_VREF = OFF_SC + ST * 256;  // [ST][2]
-    static constexpr int OFF_RED = OFF_VREF + 32;       // [ROWS][4 warps]
-    static constexpr int OFF_ROW = OFF_RED + 16 * ROWS;  // [ROWS] logit factor, reference
-    static constexpr int OFF_LIM = OFF_ROW + 8 * ROWS;   // [ROWS] keys a row sees: from, to
-    static constexpr int OFF_TOP = OFF_LIM + 8 * ROWS;   // [ROWS] next reference, as ordered int
-    static constexpr int OFF_VRUN = OFF_TOP + 4 * ROWS;  // [2 halves] vrun, its log2, 1 / vrun
-    static constexpr int OFF_BAR = OFF_VRUN + 32;
-    static constexpr int N_BAR = 5 * ST + 3;
+    static constexpr int OFF_SC = OFF_P + 2 * N * 128;  // [STV][K, V][2 halves][8 groups]
+    static constexpr int OFF_RED = OFF_SC + STV * 128;  // [ROWS][4 warps]
+    static constexpr int OFF_ROW = OFF_RED + 16 * ROWS;  // [2][2][ROWS] logit factor, reference
+    static constexpr int OFF_LIM = OFF_ROW + 32 * ROWS;  // [2][ROWS] keys a row sees: from, to
+    static constexpr int OFF_TOP = OFF_LIM + 16 * ROWS;  // [2][ROWS] next reference, ordered int
+    static constexpr int OFF_VRUN = OFF_TOP + 8 * ROWS;  // [2][2 halves] vrun, log2, 1 / vrun
+    static constexpr int OFF_OUT = OFF_VRUN + 64;        // [2][ROWS] a row's position (-1: none) and head
+    static constexpr int OFF_SEG = OFF_OUT + 16 * ROWS;  // [8] Kv8Segment
+    static constexpr int OFF_BAR = OFF_SEG + 8 * 64;
+    static constexpr int N_BAR = 2 * STK + 3 * STV + 8;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
     static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
     static constexpr int TMEM_COLS = N == 16 ? 64 : 4 * N;  // two of S^T, one of O^T
@@ -137,30 +139,101 @@ __device__ __forceinline__ Kv8Keys kv8_keys(const Kv8DecodeParams& p, const Kv8S
     return k;
 }
 
-// A CTA's walk over its range of tiles: segments of consecutive items.
+// Tiles are numbered with 31 bits (the host refuses more).  `tiles` of them go to `teams`
+// teams, at most as many: team t starts at floor(tiles * t / teams).
+__device__ __forceinline__ int kv8_range_start(int tiles, int team, int teams) {
+    const int each = tiles / teams, rest = tiles - each * teams;
+    return each * team + rest * team / teams;
+}
+
+// A warp's walk over its CTA's range of tiles: segments of consecutive items.  The lanes
+// hold the lengths of 32 sequences, so a step to the next one seldom reads memory.
 template <int SUB>
 struct Kv8Walk {
     int b, hs, u;        // the item: sequence, set of `width` head groups, row unit
     int off;             // its tiles already passed
-    long long left;      // tiles of this CTA still to come
+    int left;            // tiles of this CTA still to come
+    int base;            // lane l holds sequence base + l
+    Kv8Seq held;
     Kv8Seq seq;
     Kv8Keys keys;
     int n;               // its tiles
+    __device__ __forceinline__ void hold(const Kv8DecodeParams& p, int base_) {
+        base = base_;
+        const int mine = base + int(threadIdx.x & 31);
+        held = {0, 0, 0};
+        if (mine < p.B) held = kv8_seq(p, mine);
+    }
     __device__ __forceinline__ void load(const Kv8DecodeParams& p) {
+        if (b - base >= 32) hold(p, b);
+        const int l = b - base;
+        seq.q0 = __shfl_sync(0xffffffffu, held.q0, l);
+        seq.n = __shfl_sync(0xffffffffu, held.n, l);
+        seq.len = __shfl_sync(0xffffffffu, held.len, l);
         keys = kv8_keys<SUB>(p, seq, u);
         n = keys.tiles();
     }
-    __device__ __forceinline__ void start(const Kv8DecodeParams& p, int b_, int hs_, int u_,
-                                          int off_, long long left_) {
-        b = b_, hs = hs_, u = u_, off = off_, left = left_;
-        if (left > 0) {
-            seq = kv8_seq(p, b);
+    __device__ __forceinline__ int held_tiles(const Kv8DecodeParams& p) const {
+        int t = 0;
+        for (int v = 0; v < p.units; ++v) t += kv8_keys<SUB>(p, held, v).tiles();
+        return t * (p.groups / p.width);
+    }
+    // Adds up the tiles of one head group (the result) and goes to the first of the range
+    // of team `team` of `teams`; start: that tile's number.
+    __device__ __forceinline__ int find(const Kv8DecodeParams& p, int team, int& teams,
+                                        int& start) {
+        const int sets = p.groups / p.width, lane = threadIdx.x & 31;
+        hold(p, 0);
+        int t = held_tiles(p), all = t;
+        for (int x = 32; x < p.B; x += 32) {
+            hold(p, x);
+            all += held_tiles(p);
+        }
+        all = __reduce_add_sync(0xffffffffu, all);
+        teams = max(min(all, p.teams), 1);
+        left = start = 0;
+        if (team >= teams || all == 0) return all;
+        start = kv8_range_start(all, team, teams);
+        left = kv8_range_start(all, team + 1, teams) - start;
+        if (p.B > 32) {
+            hold(p, 0);
+            t = held_tiles(p);
+        }
+        off = start;
+        hs = u = 0;
+        while (true) {  // 32 sequences at a time
+            int inc = t;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, inc, x);
+                if (lane >= x) inc += o;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, off < inc);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                b = base + l;
+                off -= __shfl_sync(0xffffffffu, inc - t, l);
+                t = __shfl_sync(0xffffffffu, t, l);
+                break;
+            }
+            off -= __shfl_sync(0xffffffffu, inc, 31);
+            hold(p, base + 32);
+            t = held_tiles(p);
+        }
+        if (sets > 1) {
+            t /= sets;
+            hs = off / t;
+            off -= hs * t;
+        }
+        load(p);
+        while (off >= n) {
+            off -= n;
+            ++u;
             load(p);
         }
+        return all;
     }
-    __device__ __forceinline__ int segment() const {
-        return int(min((long long)(n - off), left));
-    }
+    __device__ __forceinline__ int segment() const { return min(n - off, left); }
     __device__ __forceinline__ void next(const Kv8DecodeParams& p) {
         left -= segment();
         off = 0;
@@ -170,7 +243,7 @@ struct Kv8Walk {
                 u = 0;
                 if (++hs == p.groups / p.width) {
                     hs = 0;
-                    seq = kv8_seq(p, ++b);
+                    ++b;
                 }
             }
             load(p);
@@ -178,16 +251,16 @@ struct Kv8Walk {
     }
 };
 
-// Teams with work (a tile each at least), and the first tile of one
-__device__ __forceinline__ int kv8_teams(long long tiles, int teams) {
-    return int(min(tiles, (long long)teams));
-}
-__device__ __forceinline__ long long kv8_div(long long x, long long y) {  // x >= 0, y > 0
-    return ((x | y) >> 32) == 0 ? (long long)(uint32_t(x) / uint32_t(y)) : x / y;
-}
-__device__ __forceinline__ long long kv8_range_start(long long tiles, int team, int teams) {
-    return kv8_div(tiles * team, teams);
-}
+// What the consumers need to know of a CTA's consecutive tiles of one item
+struct Kv8Segment {
+    int tiles, first;  // tiles here (0: no more segments), the first one's number
+    int b, hg, u;      // the item
+    int slot;          // this CTA's partial of it; -1: the item is whole
+    Kv8Seq seq;
+    Kv8Keys keys;
+};
+static_assert(sizeof(Kv8Segment) <= 64, "");
+
 // float bits as an int that orders like the float, and back
 __device__ __forceinline__ int ordered(float x) {
     const int i = __float_as_int(x);
@@ -312,15 +385,14 @@ __device__ __forceinline__ bool kv8_row(const Kv8DecodeParams& p, const Kv8Seq& 
     return i < s.n && kvh < p.Hkv;
 }
 
-// Dimension `dim` (0..127, of both heads of a pair) of a finished row: its sum over the
-// keys of weights (relative to 2^ref) times values, and of weights
+// Dimension `dim` (0..127, of both heads of a pair) of a finished row r, position i of its
+// sequence and query head h: from its sums over the keys of weights (relative to 2^ref)
+// times values, and of weights
 template <int ROWS, bool PAIR>
 __device__ __forceinline__ void kv8_store(const Kv8DecodeParams& p, const Kv8Seq& seq, int b,
-                                          int hg, int u, int r, int dim, float acc, float sum,
+                                          int i, int h, int r, int dim, float acc, float sum,
                                           float ref) {
     constexpr int D = PAIR ? 64 : 128;
-    int i, h;
-    if (!kv8_row<ROWS, PAIR>(p, seq, hg, u, r, i, h)) return;
     if (!PAIR || dim / 64 == r / (ROWS / 2))
         p.out[(size_t(seq.q0 + i) * p.Hq + h) * D + (dim & (D - 1))] =
             __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
@@ -342,27 +414,26 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full_k = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* full_v = full_k + C::ST;
-    uint64_t* full_s = full_v + C::ST;   // scales
-    uint64_t* s_done = full_s + C::ST;   // S^T computed: its K stage is free
-    uint64_t* o_done = s_done + C::ST;   // O^T summed: its V stage, scales and P are free
-    uint64_t* p_ready = o_done + C::ST;  // [2] P written, S^T read
-    uint64_t* q_ready = p_ready + 2;     // a segment's q written
+    uint64_t* s_done = full_k + C::STK;  // S^T computed: its K stage is free
+    uint64_t* full_v = s_done + C::STK;
+    uint64_t* full_s = full_v + C::STV;  // scales
+    uint64_t* o_done = full_s + C::STV;  // O^T summed: its V stage, scales and P are free
+    uint64_t* p_ready = o_done + C::STV;  // [2] P written, S^T read
+    uint64_t* seg_ready = p_ready + 2;   // [2] a segment's description written
+    uint64_t* seg_free = seg_ready + 2;  // [2] the segment is finished
+    uint64_t* q_ready = seg_free + 2;    // [2] the segment's q written
     int* misc = reinterpret_cast<int*>(smem + C::OFF_MISC);
     volatile int* abort_flag = misc;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
-    volatile int* first_item = misc + 2;                                   // b, hs, u, off
-    volatile long long* range = reinterpret_cast<volatile long long*>(misc + 6);  // left, first tile; all tiles
-    long long* scan = reinterpret_cast<long long*>(smem + C::OFF_P);       // before P is used
+    Kv8Segment* segments = reinterpret_cast<Kv8Segment*>(smem + C::OFF_SEG);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
         for (int i = 0; i < C::N_BAR; ++i) mbar_init(full_k + i, 1);
         *abort_flag = 0;
-        range[0] = 0;
         fence_mbar_init();
     }
-    if (warp == PRODUCER) {
+    if (warp == PRODUCER + 1) {
         tmem_alloc(tmem_slot, C::TMEM_COLS);
         tmem_relinquish();  // at once: the SM's other CTAs cannot allocate before
         if (lane == 0) {
@@ -370,152 +441,172 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             tma_prefetch_desc(&tm_v);
         }
     }
-    griddep_launch_dependents();
     griddep_wait();  // whatever wrote the cache, the tables and q has completed
 
-    // Every CTA adds up the tiles of one head group and finds the item its range starts in.
-    const int team = blockIdx.x / p.width, member = blockIdx.x - team * p.width;
-    {
-        const int sets = p.groups / p.width;
-        const int per = (p.B + C::THREADS - 1) / C::THREADS;
-        const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-        auto tiles_of = [&](int b) {
-            const Kv8Seq s = kv8_seq(p, b);
-            long long t = 0;
-            for (int u = 0; u < p.units; ++u) t += kv8_keys<SUB>(p, s, u).tiles();
-            return t;
-        };
-        long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += tiles_of(b) * sets;
-        long long inc = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += o;
-        }
-        if (lane == 31) scan[warp] = inc;
-        __syncthreads();
-        long long before = inc - mine, all = 0;
-        for (int w = 0; w < C::THREADS / 32; ++w) {
-            if (w < warp) before += scan[w];
-            all += scan[w];
-        }
-        const int teams = kv8_teams(all, p.teams);
-        const bool works = team < teams;
-        const long long lo = works ? kv8_range_start(all, team, teams) : 0;
-        const long long hi = works ? kv8_range_start(all, team + 1, teams) : 0;
-        if (lo < hi && lo >= before && lo < before + mine) {
-            long long at = lo - before;
-            int b = b0;
-            long long t = tiles_of(b);
-            while (at >= t * sets) {
-                at -= t * sets;
-                t = tiles_of(++b);
-            }
-            const int hs = sets > 1 ? int(at / t) : 0;
-            at -= hs * t;
-            const Kv8Seq s = kv8_seq(p, b);
-            int u = 0, n = kv8_keys<SUB>(p, s, 0).tiles();
-            while (at >= n) {
-                at -= n;
-                n = kv8_keys<SUB>(p, s, ++u).tiles();
-            }
-            first_item[0] = b;
-            first_item[1] = hs;
-            first_item[2] = u;
-            first_item[3] = int(at);
-            range[0] = hi - lo;
-            range[1] = lo;
-            range[2] = all;
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Kv8Walk<SUB> walk;
-    walk.start(p, first_item[0], first_item[1], first_item[2], first_item[3], range[0]);
 
     if (warp == PRODUCER) {
         // ------------------------------------------------------------ producer
         // A tile is one copy per page it touches (128 rows at most), one lane each, and the
-        // scales of its eight groups of 16 keys (a scale block is 16 keys or more): lane
-        // 8 * half + group fetches those of its group.  Their loads are under way while the
-        // lanes wait for free stages.
+        // scales of its eight groups of 16 keys (a scale block is 16 keys or more) of each
+        // head.  The warp looks the pages of a batch of tiles up at once, a lane for each
+        // tile and box and for each tile, head and group, one batch ahead and across
+        // segments; what it then needs of global memory goes to shared memory by itself
+        // (bulk copies, and asynchronous copies of the scales), so no load holds it up.
+        const int team = blockIdx.x / p.width, member = blockIdx.x - team * p.width;
+        Kv8Walk<SUB> walk;
+        int teams, range;
+        const int all = walk.find(p, team, teams, range);
+        const int total = walk.left;
+        constexpr int BATCH = PAIR ? 2 : 4;
         const int box = min(1 << p.page_shift, 128), boxes = 128 / box;
-        const int half = (lane >> 3) & 1, grp = lane & 7;
-        int c = 0, copies[2] = {0, 0};  // tiles; copies of K and of V issued
+        const int mine = lane * BATCH / 32;  // this lane's tile of a batch
+        const int half = PAIR ? (lane >> 3) & 1 : 0, grp = lane & 7;
+        struct Batch {
+            int t, t1;   // its tiles (none: no more batches)
+            int seg;     // their segment, if they are its first, else -1
+            int lo, hi;  // the segment's keys
+            int b, hg;   // and its sequence and head group
+        };
+        Batch seg_now = {0, 0, -1, 0, 0, 0, 0};  // what is left of the segment being cut up
+        int segs = 0;
+        auto next_batch = [&](Batch& x) {
+            if (seg_now.t >= seg_now.t1) {
+                if (walk.left <= 0) {
+                    x.t = x.t1 = 0;
+                    x.seg = -1;
+                    return;
+                }
+                Kv8Segment g;
+                g.tiles = walk.segment();
+                g.first = walk.keys.first() + walk.off;
+                g.b = walk.b, g.hg = walk.hs * p.width + member, g.u = walk.u;
+                g.seq = walk.seq, g.keys = walk.keys;
+                const bool starts = walk.off == 0, whole = starts && g.tiles == walk.n;
+                g.slot = whole ? -1 : segs == 0 ? 0 : 1;
+                if (starts && !whole && lane == 0) {
+                    // for the combine: the item, the teams it is in (the one with its last
+                    // tile is where it ends), and this CTA's partial
+                    const int end = range + (total - walk.left) + walk.n;
+                    const int parts = int(((long long)end * teams - 1) / all) - team + 1;
+                    p.cut[blockIdx.x] = make_int4(g.b, g.hg, g.u, 2 * parts + g.slot);
+                }
+                // (eight slots: at most two segments ahead of the batch that is copied, and
+                // that one's segment waits for the last but one before it)
+                if (lane == 0) segments[segs & 7] = g;
+                seg_now = {g.first, g.first + g.tiles, segs++, g.keys.lo, g.keys.hi, g.b, g.hg};
+                walk.next(p);
+            }
+            x = seg_now;
+            x.t1 = min(x.t + BATCH, x.t1);
+            seg_now.t = x.t1;
+            seg_now.seg = -1;
+        };
+        // Rows without a visible key are read from a page that has one: their own table entry
+        // may name no page.
+        auto copies = [&](const Batch& x) { return x.t + mine < x.t1 && half == 0 && grp < boxes; };
+        auto seen = [&](const Batch& x) {
+            const int a = (x.t + mine) * 128 + grp * 16;
+            return x.t + mine < x.t1 && a < x.hi && a + 16 > x.lo &&
+                   (PAIR ? 2 * x.hg + half : x.hg) < p.Hkv;
+        };
+        int box_page = 0, grp_page = 0;  // of the batch looked up last, this lane's
+        auto look_up = [&](const Batch& x) {
+            const int* row = p.block_table + size_t(x.b) * p.max_pages;
+            const int t = x.t + mine, a = t * 128 + grp * box;
+            const int key = a < x.hi && a + box > x.lo ? a : max(x.lo, t * 128);
+            // (a lane without a box or a group reads the row's first entry, and uses none)
+            box_page = __ldg(row + (copies(x) ? key >> p.page_shift : 0));
+            grp_page = __ldg(row + (seen(x) ? (t * 128 + grp * 16) >> p.page_shift : 0));
+        };
+        auto slot = [&](int page, int at) {
+            if (page < 0 || page >= p.num_pages) {
+                raise_device_error(kDevBadKvIndex);
+                page = 0;
+            }
+            return (page << p.page_shift) + (at & ((1 << p.page_shift) - 1));
+        };
+        int c = 0, copied[2] = {0, 0};  // tiles; copies of K and of V issued
         bool ok = true;
-        for (; walk.left > 0 && ok; walk.next(p)) {
-            const int* row = p.block_table + size_t(walk.b) * p.max_pages;
-            const int hg = walk.hs * p.width + member;
-            const int x = hg * 128;
-            const int kvh = PAIR ? 2 * hg + half : hg;
-            const bool here = lane < (PAIR ? 16 : 8) && kvh < p.Hkv;
-            const int t1 = walk.keys.first() + walk.off + walk.segment();
-            for (int t = walk.keys.first() + walk.off; t < t1 && ok; ++t, ++c) {
-                auto slot_of = [&](int key, int at) {  // row `at` of the page that holds `key`
-                    int page = __ldg(row + (key >> p.page_shift));
-                    if (page < 0 || page >= p.num_pages) {
-                        raise_device_error(kDevBadKvIndex);
-                        page = 0;
-                    }
-                    return (page << p.page_shift) + (at & ((1 << p.page_shift) - 1));
-                };
-                int z = 0;
-                if (lane < boxes) {
-                    // rows without a visible key are read from a page that has one: their
-                    // own table entry may name no page
-                    const int a = t * 128 + lane * box;
-                    const bool seen = a < walk.keys.hi && a + box > walk.keys.lo;
-                    z = slot_of(seen ? a : max(walk.keys.lo, t * 128), a);
-                }
-                const int a = t * 128 + grp * 16;
-                float ks = 0.f, vs = 0.f;
-                if (here && a < walk.keys.hi && a + 16 > walk.keys.lo) {
-                    const size_t at = size_t(slot_of(a, a) >> p.sb_shift) * p.Hkv + kvh;
-                    ks = __ldg(p.k_scale + at);
-                    vs = __ldg(p.v_scale + at);
-                }
-                const int s = c % C::ST;
-                const uint32_t ph = ((c / C::ST) & 1) ^ 1;
-                ok = mbar_wait_warp(s_done + s, ph, abort_flag);
+        Batch now;
+        if (lane == 0) p.cut[blockIdx.x].x = -1;  // unless an item is cut
+        __syncwarp();
+        next_batch(now);
+        if (lane == 0 && now.seg == 0) mbar_arrive(seg_ready);
+        if (now.t < now.t1) look_up(now);
+        while (now.t < now.t1) {
+            const bool copies_now = copies(now), seen_now = seen(now);
+            int z = 0;               // first row of this lane's box
+            size_t scale_at = 0;     // where this lane's group's scales are
+            if (copies_now) z = slot(box_page, (now.t + mine) * 128 + grp * box);
+            if (seen_now)
+                scale_at = size_t(slot(grp_page, (now.t + mine) * 128 + grp * 16) >> p.sb_shift) *
+                               p.Hkv +
+                           (PAIR ? 2 * now.hg + half : now.hg);
+            Batch next;
+            next_batch(next);
+            if (next.t < next.t1) look_up(next);
+            if (now.seg > 0) {
+                const int buf = now.seg & 1;
+                ok = mbar_wait_warp(seg_free + buf, ((now.seg >> 1) & 1) ^ 1, abort_flag);
                 if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(full_k + s, C::TILE);
+                if (lane == 0) mbar_arrive(seg_ready + buf);
                 __syncwarp();
-                if (lane < boxes)
-                    tma_load_2d(smem + C::OFF_K + s * C::TILE + lane * box * 128, &tm_k,
-                                full_k + s, x, z);
-                ++copies[0];
-                ok = mbar_wait_warp(o_done + s, ph, abort_flag);
+            }
+            for (int t = now.t; t < now.t1; ++t, ++c) {
+                const bool turn = mine == t - now.t;  // this lane's tile
+                float ks = 0.f, vs = 0.f;
+                if (turn && seen_now) {
+                    ks = __ldg(p.k_scale + scale_at);
+                    vs = __ldg(p.v_scale + scale_at);
+                }
+                const int sk = c % C::STK, s = c % C::STV;
+                ok = mbar_wait_warp(s_done + sk, ((c / C::STK) & 1) ^ 1, abort_flag);
+                if (!ok) break;
+                if (lane == 0) mbar_arrive_expect_tx(full_k + sk, C::TILE);
+                __syncwarp();
+                if (turn && copies_now)
+                    tma_load_2d(smem + C::OFF_K + sk * C::TILE + grp * box * 128, &tm_k,
+                                full_k + sk, now.hg * 128, z);
+                ++copied[0];
+                ok = mbar_wait_warp(o_done + s, ((c / C::STV) & 1) ^ 1, abort_flag);
                 if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(full_v + s, C::TILE);
                 __syncwarp();
-                if (lane < boxes)
-                    tma_load_2d(smem + C::OFF_V + s * C::TILE + lane * box * 128, &tm_v,
-                                full_v + s, x, z);
-                ++copies[1];
+                if (turn && copies_now)
+                    tma_load_2d(smem + C::OFF_V + s * C::TILE + grp * box * 128, &tm_v,
+                                full_v + s, now.hg * 128, z);
+                ++copied[1];
                 // V's stage being free, so is the stage of scales: every consumer warp has
-                // read them before that tile's P V was issued
-                float vref = vs;
-#pragma unroll
-                for (int off = 4; off > 0; off >>= 1)
-                    vref = fmaxf(vref, __shfl_xor_sync(0xffffffffu, vref, off));
-                if (lane < 16)
-                    reinterpret_cast<float4*>(smem + C::OFF_SC)[s * 16 + lane] =
-                        make_float4(ks, __log2f(vs), vs, 0.f);
-                if (lane < 16 && grp == 0)
-                    reinterpret_cast<float*>(smem + C::OFF_VREF)[s * 2 + half] = vref;
+                // read them before that tile's P V was issued.  Groups without a visible key
+                // get scales of 0.
+                if (turn) {
+                    float* sc =
+                        reinterpret_cast<float*>(smem + C::OFF_SC) + s * 32 + half * 8 + grp;
+                    sc[0] = ks, sc[16] = vs;
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full_s + s);
             }
+            if (!ok) break;
+            now = next;
+        }
+        // no more segments
+        if (ok && mbar_wait_warp(seg_free + (segs & 1), ((segs >> 1) & 1) ^ 1, abort_flag) &&
+            lane == 0) {
+            segments[segs & 7].tiles = 0;
+            mbar_arrive(seg_ready + (segs & 1));
         }
         // every issued copy lands before the CTA may release the memory
         if (lane == 0) {
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv)
-                for (int s = 0; s < C::ST; ++s) {
-                    const int n = copies[kv] / C::ST + (s < copies[kv] % C::ST ? 1 : 0);
+                for (int s = 0; s < (kv ? C::STV : C::STK); ++s) {
+                    const int st = kv ? C::STV : C::STK;
+                    const int n = copied[kv] / st + (s < copied[kv] % st ? 1 : 0);
                     const uint64_t t0 = globaltimer_ns();
                     while (n > 0 && !mbar_try_wait((kv ? full_v : full_k) + s, (n - 1) & 1))
                         if (globaltimer_ns() - t0 > kWaitLimitNs) {
@@ -539,32 +630,34 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             const uint64_t dp = mn_chunk_desc(smem_u32(smem + C::OFF_P), 128, 2048);
             int x = 0, y = 0;  // next tile of S^T, of P V
             bool ok = true;
-            for (int segment = 0; walk.left > 0 && ok; walk.next(p), ++segment) {
-                const int first = y, end = y + walk.segment();
-                ok = mbar_wait(q_ready, segment & 1, abort_flag);
+            for (int seg = 0; ok; ++seg) {
+                ok = mbar_wait(q_ready + (seg & 1), (seg >> 1) & 1, abort_flag);
+                const int tiles = ok ? segments[seg & 7].tiles : 0;
+                if (tiles == 0) break;
+                const int first = y, end = y + tiles;
                 uint64_t since = globaltimer_ns();  // of the last issue, as the clock checks see it
                 int polls = 0, issued = x + y;
                 while (ok && y < end) {
-                    if (x < end && x < y + 2 && mbar_test(full_k + x % C::ST, (x / C::ST) & 1)) {
+                    if (x < end && x < y + 2 && mbar_test(full_k + x % C::STK, (x / C::STK) & 1)) {
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_ss_f8(tmem + (x & 1) * C::N,
-                                       dk + (((x % C::ST) * C::TILE + kk * 32) >> 4),
+                                       dk + (((x % C::STK) * C::TILE + kk * 32) >> 4),
                                        dq + ((kk * 32) >> 4), idesc_s, kk > 0);
-                        umma_commit(s_done + x % C::ST);
+                        umma_commit(s_done + x % C::STK);
                         ++x;
                     }
                     if (y < x && mbar_test(p_ready + (y & 1), (y >> 1) & 1) &&
-                        mbar_test(full_v + y % C::ST, (y / C::ST) & 1)) {
+                        mbar_test(full_v + y % C::STV, (y / C::STV) & 1)) {
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
                             umma_ss_f8(tmem + 2 * C::N,
-                                       dv + (((y % C::ST) * C::TILE + kk * 32 * 128) >> 4),
+                                       dv + (((y % C::STV) * C::TILE + kk * 32 * 128) >> 4),
                                        dp + (((y & 1) * (C::N * 128) + kk * 512) >> 4), idesc_o,
                                        y > first || kk > 0);
-                        umma_commit(o_done + y % C::ST);
+                        umma_commit(o_done + y % C::STV);
                         ++y;
                     }
                     if ((++polls & 63) == 0) {
@@ -591,12 +684,12 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         const uint32_t sp = smem_u32(smem + C::OFF_P) + t128 * 16;
         const uint32_t t_s = tmem + (uint32_t((warp & 3) * 32) << 16);  // this warp's lanes
         const uint32_t t_o = t_s + 2 * C::N;
-        const uint32_t sq = smem_u32(smem + C::OFF_Q);
         float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
-        float2* rows = reinterpret_cast<float2*>(smem + C::OFF_ROW);
-        int2* limits = reinterpret_cast<int2*>(smem + C::OFF_LIM);
-        int* next_ref = reinterpret_cast<int*>(smem + C::OFF_TOP);
-        float4* vrun = reinterpret_cast<float4*>(smem + C::OFF_VRUN);  // vrun, log2, 1 / vrun
+        float2* const all_rows = reinterpret_cast<float2*>(smem + C::OFF_ROW);
+        int2* const all_limits = reinterpret_cast<int2*>(smem + C::OFF_LIM);
+        int* const all_next = reinterpret_cast<int*>(smem + C::OFF_TOP);
+        int2* const all_out = reinterpret_cast<int2*>(smem + C::OFF_OUT);
+        float4* const all_vrun = reinterpret_cast<float4*>(smem + C::OFF_VRUN);
         float* so = reinterpret_cast<float*>(smem + C::OFF_P);  // [ROWS][128], P unused
         const int my_half = PAIR ? t128 >> 6 : 0;  // of this thread's dimension
         // the KV heads (of a pair) of this warpgroup's rows: half0 and, with NH = 2, half0 + 1
@@ -604,86 +697,122 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         const int half0 = PAIR && C::WGS == 2 ? wg : 0;
         auto half_of = [](int r) { return NH == 2 ? r / SUB : 0; };  // of row R0 + r
         int c = 0;
-        bool aborted = false, first_segment = true;
-        for (; walk.left > 0; walk.next(p), first_segment = false) {
-            const int hg = walk.hs * p.width + member;
-            const int segment = walk.segment();
-            const bool whole = walk.off == 0 && segment == walk.n;
-            // --- q rows of this item as two e4m3 terms; the MMAs that read the last
-            // item's rows have completed
-            for (int r = warp; r < ROWS; r += CT / 32) {
-                int i, h;
-                const bool valid = kv8_row<ROWS, PAIR>(p, walk.seq, hg, walk.u, r, i, h);
-                constexpr int D = PAIR ? 64 : 128;
+        // After a wait that gave up (device error word set) a warp waits no more, so that all
+        // come to the same barriers; what it computes is thrown away.
+        bool dead = false;
+        bool dry = true;
+        auto wait = [&](uint64_t* bar, int phase) {
+            if (!dead && !dry) dead = !mbar_wait_warp(bar, phase & 1, abort_flag);
+        };
+        auto wait_o = [&](int x) { wait(o_done + x % C::STV, x / C::STV); };  // P V of tile x
+        int gen = 0;  // which of the two copies of the rows' references and of vrun is in use
+        // Writes segment seg's q rows as two e4m3 terms; false: there is none.
+        auto stage_q = [&](int seg) {
+            const int buf = seg & 1;
+            wait(seg_ready + buf, seg >> 1);
+            if (consumers_any<CT>(dead)) return false;
+            const Kv8Segment& g = segments[seg & 7];
+            const bool any = g.tiles > 0;
+            if (any) {
+                constexpr int D = PAIR ? 64 : 128, MINE = ROWS * 32 / CT;  // rows of a warp
+                const uint32_t sq = smem_u32(smem + C::OFF_Q);  // its last S^T has been read
                 const int d0 = PAIR ? (lane * 4) & 63 : lane * 4;
-                const bool in = valid && (!PAIR || (lane >> 4) == r / SUB);
-                uint2 w = make_uint2(0u, 0u);
-                if (in)
-                    w = __ldg(reinterpret_cast<const uint2*>(
-                        p.q + (size_t(walk.seq.q0 + i) * p.Hq + h) * D + d0));
-                const uint32_t big = max(max((w.x << 16) & 0x7fffffffu, w.x & 0x7fff0000u),
-                                         max((w.y << 16) & 0x7fffffffu, w.y & 0x7fff0000u));
-                const uint32_t amax = __reduce_max_sync(0xffffffffu, big);
-                // power-of-two factor that brings the row's largest |q| to [128, 256)
-                const int e = max(int(amax >> 23), 8);
-                const float up = __uint_as_float(uint32_t(261 - e) << 23);
-                uint32_t hi, lo;
-                split_e4m3x4(bf16_lo(w.x) * up, bf16_hi(w.x) * up, bf16_lo(w.y) * up,
-                             bf16_hi(w.y) * up, 16.f, hi, lo);
-                auto put = [&](int n, uint32_t codes) {  // row n of the operand, this lane's dims
-                    const uint32_t at = (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4;
-                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(sq + n * 128 + at), "r"(codes)
-                                 : "memory");
-                };
-                put(r, hi);
-                put(ROWS + r, lo);
-                // a row with an infinity or a NaN has no factor: its logits are NaN
-                if (lane == 0) {
-                    const int end = walk.seq.len - walk.seq.n + i + 1;
-                    limits[r] = make_int2(p.window > 0 ? end - p.window : 0,
-                                          min(end, walk.keys.hi));
-                    next_ref[r] = ordered(kNoKey);
-                    rows[r] = make_float2(
-                        amax >= 0x7f800000u
-                            ? NAN
-                            : __uint_as_float(uint32_t(e - 7) << 23) * p.scale_log2,
-                        kNoKey);
+                uint2 w[MINE];
+#pragma unroll
+                for (int j = 0; j < MINE; ++j) {
+                    const int r = warp * MINE + j;
+                    int i, h;
+                    const bool valid = kv8_row<ROWS, PAIR>(p, g.seq, g.hg, g.u, r, i, h);
+                    w[j] = make_uint2(0u, 0u);
+                    if (valid && (!PAIR || (lane >> 4) == r / SUB))
+                        w[j] = __ldg(reinterpret_cast<const uint2*>(
+                            p.q + (size_t(g.seq.q0 + i) * p.Hq + h) * D + d0));
+                    if (lane == 0) {
+                        const int end = g.seq.len - g.seq.n + i + 1;
+                        all_limits[buf * ROWS + r] =
+                            make_int2(p.window > 0 ? end - p.window : 0, min(end, g.keys.hi));
+                        all_next[buf * ROWS + r] = ordered(kNoKey);
+                        all_out[buf * ROWS + r] = make_int2(valid ? i : -1, h);
+                    }
                 }
+#pragma unroll
+                for (int j = 0; j < MINE; ++j) {
+                    const int r = warp * MINE + j;
+                    const uint32_t big =
+                        max(max((w[j].x << 16) & 0x7fffffffu, w[j].x & 0x7fff0000u),
+                            max((w[j].y << 16) & 0x7fffffffu, w[j].y & 0x7fff0000u));
+                    const uint32_t amax = __reduce_max_sync(0xffffffffu, big);
+                    // power-of-two factor that brings the row's largest |q| to [128, 256)
+                    const int e = max(int(amax >> 23), 8);
+                    const float up = __uint_as_float(uint32_t(261 - e) << 23);
+                    uint32_t hi, lo;
+                    split_e4m3x4(bf16_lo(w[j].x) * up, bf16_hi(w[j].x) * up,
+                                 bf16_lo(w[j].y) * up, bf16_hi(w[j].y) * up, 16.f, hi, lo);
+                    auto put = [&](int n, uint32_t codes) {  // operand row n, this lane's dims
+                        const uint32_t at = (((lane >> 2) ^ (n & 7)) << 4) + (lane & 3) * 4;
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(sq + n * 128 + at),
+                                     "r"(codes)
+                                     : "memory");
+                    };
+                    put(r, hi);
+                    put(ROWS + r, lo);
+                    // a row with an infinity or a NaN has no factor: its logits are NaN
+                    if (lane == 0)
+                        all_rows[(buf * 2 + gen) * ROWS + r] = make_float2(
+                            amax >= 0x7f800000u
+                                ? NAN
+                                : __uint_as_float(uint32_t(e - 7) << 23) * p.scale_log2,
+                            kNoKey);
+                }
+                fence_proxy_async();
             }
-            fence_proxy_async();
             consumers_sync<CT>();
-            if (tid == 0) mbar_arrive(q_ready);
-
+            if (tid == 0) mbar_arrive(q_ready + buf);
+            return any;
+        };
+        // Segment -1 is a dry run of one tile on whatever tensor and shared memory hold, with
+        // no waits and nothing handed on: it brings the instructions of a tile into the SM's
+        // cache while the first keys are on their way (a kernel starts with none of them,
+        // and fetching them costs up to 3 us).
+        bool more = true;
+        for (int seg = -1; more; ++seg) {
+            const Kv8Segment& g = segments[seg & 7];
+            const int segment = dry ? 1 : g.tiles;
+            const int2* const limits = all_limits + (seg & 1) * ROWS;
+            int* const next_ref = all_next + (seg & 1) * ROWS;
+            const Kv8Keys keys = g.keys;
             float l[RW];
 #pragma unroll
             for (int r = 0; r < RW; ++r) l[r] = 0.f;
             // keys that every row sees, in tiles between which no mask is needed
-            const int t0 = walk.keys.first() + walk.off;
-            const int last = walk.seq.len - walk.seq.n;  // position of query 0
-            const int i_lo = walk.u * SUB / p.G;
-            const int i_hi = min((walk.u * SUB + SUB - 1) / p.G, walk.seq.n - 1);
+            const int t0 = dry ? 0 : g.first;
+            const int last = g.seq.len - g.seq.n;  // position of query 0
+            const int i_lo = g.u * SUB / p.G;
+            const int i_hi = min((g.u * SUB + SUB - 1) / p.G, g.seq.n - 1);
             const int all_hi = last + i_lo + 1;
             const int all_lo = p.window > 0 ? max(last + i_hi + 1 - p.window, 0) : 0;
-            auto wait_o = [&](int x) {  // P V of tile x (counted over the CTA) has completed
-                return mbar_wait_warp(o_done + x % C::ST, (x / C::ST) & 1, abort_flag);
-            };
             for (int t = t0; t < t0 + segment; ++t, ++c) {
-                const int s = c % C::ST;
-                const uint32_t ph = (c / C::ST) & 1;
-                bool ok = true;
+                const int s = c % C::STV;
+                const float2* rows = all_rows + ((seg & 1) * 2 + gen) * ROWS;
+                const float4* vrun = all_vrun + gen * 2;
                 const int key = t * 128 + t128;
-                ok &= mbar_wait_warp(full_s + s, ph, abort_flag);
-                float4 sc[NH];   // K scale, log2 of the V scale, V scale
+                wait(full_s + s, c / C::STV);
+                float4 sc[NH];   // this key's K scale, log2 of its V scale, V scale
                 float vref[NH];  // the tile's largest V scale
 #pragma unroll
                 for (int j = 0; j < NH; ++j) {
-                    sc[j] = reinterpret_cast<float4*>(
-                        smem + C::OFF_SC)[s * 16 + (half0 + j) * 8 + (t128 >> 4)];
-                    vref[j] = reinterpret_cast<float*>(smem + C::OFF_VREF)[s * 2 + half0 + j];
+                    const float* at = reinterpret_cast<const float*>(smem + C::OFF_SC) + s * 32 +
+                                      (half0 + j) * 8;
+                    const float4 a = *reinterpret_cast<const float4*>(at + 16);
+                    const float4 b = *reinterpret_cast<const float4*>(at + 20);
+                    vref[j] = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)),
+                                    fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+                    const float v = at[16 + (t128 >> 4)];
+                    sc[j] = make_float4(at[t128 >> 4], __log2f(v), v, 0.f);
                 }
                 // P's buffer is free once the tile before the last has used it
-                if (c >= 2) ok &= wait_o(c - 2);
-                ok &= mbar_wait_warp(s_done + s, ph, abort_flag);
+                if (c >= 2) wait_o(c - 2);
+                wait(s_done + c % C::STK, c / C::STK);
                 tc_fence_after();
                 const bool edge = t * 128 < all_lo || t * 128 + 128 > all_hi;
                 const uint32_t t_sc = t_s + (c & 1) * C::N;
@@ -706,9 +835,9 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 };
                 // V rows that no query sees may hold any code: a weight of 0 times NaN
                 // would still reach O
-                if (wg == 0 && (t * 128 < walk.keys.lo || t * 128 + 128 > walk.keys.hi)) {
-                    ok &= mbar_wait_warp(full_v + s, ph, abort_flag);
-                    if (key < walk.keys.lo || key >= walk.keys.hi) {
+                if (wg == 0 && !dry && (t * 128 < keys.lo || t * 128 + 128 > keys.hi)) {
+                    wait(full_v + s, c / C::STV);
+                    if (key < keys.lo || key >= keys.hi) {
                         const uint32_t v = smem_u32(smem + C::OFF_V + s * C::TILE) + t128 * 128;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) st_shared_v4(v + j * 16, 0u, 0u, 0u, 0u);
@@ -786,11 +915,12 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     }
                     fence_proxy_async();
                     tc_fence_before();
-                    if (!consumers_any<CT>(high || !ok)) break;
-                    if (t > t0) ok &= wait_o(c - 1);
-                    aborted = consumers_any<CT>(!ok);
-                    if (aborted) break;
+                    if (!consumers_any<CT>(high)) break;
+                    if (t > t0) wait_o(c - 1);
                     tc_fence_after();
+                    gen ^= 1;
+                    float2* const new_rows = all_rows + ((seg & 1) * 2 + gen) * ROWS;
+                    float4* const new_vrun = all_vrun + gen * 2;
                     float v[NH], ratio[NH];
 #pragma unroll
                     for (int j = 0; j < NH; ++j) {
@@ -816,26 +946,39 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                             tmem_st_rows<ROWS, CH>(t_o, R0 + r0, hi, lo);
                         }
                     }
-                    tc_fence_before();
-                    consumers_sync<CT>();
-                    if (tid < ROWS) rows[tid].y = unordered(next_ref[tid]);
+                    if (tid < ROWS)
+                        new_rows[tid] = make_float2(rows[tid].x, unordered(next_ref[tid]));
                     if (t128 < NH && (PAIR || wg == 0)) {
                         const float x = t128 ? v[NH - 1] : v[0];
-                        vrun[half0 + t128] =
+                        new_vrun[half0 + t128] =
                             make_float4(x, __log2f(x), x > 0.f ? 1.f / x : 0.f, 0.f);
                     }
+                    rows = new_rows;
+                    vrun = new_vrun;
+                    tc_fence_before();
                     consumers_sync<CT>();
                 }
-                if (aborted) break;
-                if (tid == 0) mbar_arrive(p_ready + (c & 1));
+                if (tid == 0 && !dry) mbar_arrive(p_ready + (c & 1));
 #pragma unroll
                 for (int r = 0; r < RW; ++r) l[r] += u[r];
             }
-            // --- end of the segment: sums over the keys, then the rows' results
-            if (!aborted) wait_o(c - 1);
+            // --- end of the segment: the next one's q, so that its first S^T can start, then
+            // this one's sums over the keys and its rows' results
+            if (dry) {
+                dry = false;
+                c = 0;
+                more = stage_q(0);
+                continue;
+            }
+            more = stage_q(seg + 1);
+            // the combine may start when every CTA has come this far, and not before: its
+            // CTAs beside these ones, waiting, cost up to a sixth of the rate
+            if (!more) griddep_launch_dependents();
+            wait_o(c - 1);
             tc_fence_after();
-            aborted = consumers_any<CT>(aborted || *abort_flag != 0);
-            const float unit = vrun[my_half].x * 0.03125f;
+            const bool lost = consumers_any<CT>(dead);
+            const float2* const rows = all_rows + ((seg & 1) * 2 + gen) * ROWS;
+            const float unit = all_vrun[gen * 2 + my_half].x * 0.03125f;
 #pragma unroll
             for (int r0 = 0; r0 < RW; r0 += CH) {
                 float hi[CH], lo[CH];
@@ -852,111 +995,121 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             }
             tc_fence_before();
             consumers_sync<CT>();
-            const long long item = ((long long)walk.b * p.groups + hg) * p.units + walk.u;
-            const size_t part = size_t(blockIdx.x) * 2 + (first_segment ? 0 : 1);
-#pragma unroll 1
+            const size_t part = size_t(blockIdx.x) * 2 + g.slot;
+#pragma unroll 2
             for (int r = R0; r < R0 + RW; ++r) {
                 const float4 x = reinterpret_cast<float4*>(red)[r];
                 float sum = (x.x + x.y) + (x.z + x.w);
                 float acc = so[r * 128 + t128];
                 // a wait gave up (device error word set): an empty result, so that no stale
                 // memory is picked up
-                if (aborted) sum = 0.f, acc = 0.f;
-                if (!whole) {
+                if (lost) sum = 0.f, acc = 0.f;
+                if (g.slot >= 0) {
                     p.part_o[(part * ROWS + r) * 128 + t128] = acc;
                     if (t128 == 0) p.part_ml[part * ROWS + r] = make_float2(rows[r].y, sum);
                 } else {
-                    kv8_store<ROWS, PAIR>(p, walk.seq, walk.b, hg, walk.u, r, t128, acc, sum,
-                                          rows[r].y);
+                    const int2 at = all_out[(seg & 1) * ROWS + r];
+                    if (at.x >= 0)
+                        kv8_store<ROWS, PAIR>(p, g.seq, g.b, at.x, at.y, r, t128, acc, sum,
+                                              rows[r].y);
                 }
             }
-            if (tid == 0 && walk.off == 0) {
-                int parts = 1;
-                if (!whole) {  // the team with the item's last tile is where it ends
-                    const long long end = range[1] + (range[0] - walk.left) + walk.n;
-                    const int teams = kv8_teams(range[2], p.teams);
-                    parts = int(kv8_div(end * teams - 1, range[2])) - team + 1;
-                }
-                p.meta[item] = make_int2(parts, 2 * team + (first_segment ? 0 : 1));
-            }
-            consumers_sync<CT>();  // red, rows and P are free again
+            consumers_sync<CT>();  // red, the segment's rows and P are free again
+            if (tid == 0) mbar_arrive(seg_free + (seg & 1));
         }
     }
+    if (warp >= PRODUCER) griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
-    if (warp == PRODUCER) {
+    if (warp == PRODUCER + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
 }
 
-// One CTA per (row, item): joins the partials of an item that several teams shared, and
-// writes the rows that no key reached.  With reference M = max_s m_s (log2 units):
-// sum = sum_s 2^(m_s - M) sum_s, O = sum_s 2^(m_s - M) O_s / sum, L = ln 2 (M + log2 sum).
-// A warp takes every eighth partial, four at a time, with an online rescaling of its own.
-constexpr int kCombineWarps = 8;
+// Joins the partials of the items that several teams shared, and writes the rows of items
+// that no key reaches.  With reference M = max_s m_s (log2 units): sum = sum_s 2^(m_s - M)
+// sum_s, O = sum_s 2^(m_s - M) O_s / sum, L = ln 2 (M + log2 sum).
+// CTA c takes the one item that CTA c of kv8_decode may have begun and not ended, and every
+// gridDim-th item's check for keys.  16 warps: several to a row, or several rows to one; a
+// warp takes four partials at a time, with an online rescaling of its own.
+constexpr int kCombineWarps = 16;
 template <int ROWS, bool PAIR>
 __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine(const Kv8DecodeParams p) {
     constexpr int SUB = PAIR ? ROWS / 2 : ROWS;
+    constexpr int WPR = ROWS < kCombineWarps ? kCombineWarps / ROWS : 1;  // warps of a row
+    constexpr int PASS = kCombineWarps / WPR;                             // rows at a time
     __shared__ __align__(16) float so[kCombineWarps][128];
     __shared__ float2 sml[kCombineWarps];
-    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t item = blockIdx.y + blockIdx.z * 65535u;
-    griddep_launch_dependents();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     griddep_wait();
-    if (item >= uint32_t(p.B) * p.groups * p.units) return;
-    const int2 meta = p.meta[item];  // (undefined for an item without tiles)
-    const uint32_t bh = item / uint32_t(p.units);
-    const int u = int(item - bh * p.units), b = int(bh / uint32_t(p.groups));
-    const int hg = int(bh - uint32_t(b) * p.groups);
+    const int4 cut = p.cut[blockIdx.x];
+    const int items = p.B * p.groups * p.units;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int bh = item / p.units, u = item - bh * p.units;
+        const int b = bh / p.groups, hg = bh - b * p.groups;
+        const Kv8Seq seq = kv8_seq(p, b);
+        if (kv8_keys<SUB>(p, seq, u).tiles() > 0) continue;
+        for (int x = tid; x < ROWS * 128; x += 32 * kCombineWarps) {
+            int i, h;
+            if (kv8_row<ROWS, PAIR>(p, seq, hg, u, x >> 7, i, h))
+                kv8_store<ROWS, PAIR>(p, seq, b, i, h, x >> 7, x & 127, 0.f, 0.f, kNoKey);
+        }
+    }
+    if (cut.x < 0) return;
+    const int b = cut.x, hg = cut.y, u = cut.z, parts = cut.w >> 1;
     const Kv8Seq seq = kv8_seq(p, b);
-    int i, h;
-    if (!kv8_row<ROWS, PAIR>(p, seq, hg, u, r, i, h)) return;
-    const int parts = kv8_keys<SUB>(p, seq, u).tiles() > 0 ? meta.x : 0;
-    if (parts == 1) return;  // one CTA has written it
-    float m = kNoKey, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const int team = meta.y >> 1, member = hg % p.width;
-    for (int x0 = warp; x0 < parts; x0 += 4 * kCombineWarps) {
-        float2 ml[4];
-        float4 o[4];
+#pragma unroll 1
+    for (int r0 = 0; r0 < ROWS; r0 += PASS) {
+        const int r = r0 + warp / WPR;
+        float m = kNoKey, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int x0 = warp % WPR; x0 < parts; x0 += 4 * WPR) {
+            float2 ml[4];
+            float4 o[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int x = x0 + j * kCombineWarps;
-            ml[j] = make_float2(kNoKey, 0.f);
-            o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (x < parts) {
-                const size_t at = (size_t((team + x) * p.width + member) * 2 +
-                                   (x == 0 ? meta.y & 1 : 0)) * ROWS + r;
-                ml[j] = p.part_ml[at];
-                o[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
+            for (int j = 0; j < 4; ++j) {
+                const int x = x0 + j * WPR;
+                ml[j] = make_float2(kNoKey, 0.f);
+                o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (x < parts) {
+                    const size_t at = (size_t(blockIdx.x + x * p.width) * 2 +
+                                       (x == 0 ? cut.w & 1 : 0)) * ROWS + r;
+                    ml[j] = p.part_ml[at];
+                    o[j] = reinterpret_cast<const float4*>(p.part_o + at * 128)[lane];
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float m1 = fmaxf(m, ml[j].x);
+                const float a = ex2_approx(m - m1), f = ex2_approx(ml[j].x - m1);
+                m = m1;
+                sum = sum * a + f * ml[j].y;
+                acc[0] = acc[0] * a + f * o[j].x;
+                acc[1] = acc[1] * a + f * o[j].y;
+                acc[2] = acc[2] * a + f * o[j].z;
+                acc[3] = acc[3] * a + f * o[j].w;
             }
         }
+        reinterpret_cast<float4*>(so[warp])[lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (lane == 0) sml[warp] = make_float2(m, sum);
+        __syncthreads();
+        for (int x = tid; x < PASS * 128; x += 32 * kCombineWarps) {
+            const int row = x >> 7, dim = x & 127;
+            int i, h;
+            if (!kv8_row<ROWS, PAIR>(p, seq, hg, u, r0 + row, i, h)) continue;
+            float M = kNoKey, total = 0.f, out = 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float m1 = fmaxf(m, ml[j].x);
-            const float a = ex2_approx(m - m1), f = ex2_approx(ml[j].x - m1);
-            m = m1;
-            sum = sum * a + f * ml[j].y;
-            acc[0] = acc[0] * a + f * o[j].x;
-            acc[1] = acc[1] * a + f * o[j].y;
-            acc[2] = acc[2] * a + f * o[j].z;
-            acc[3] = acc[3] * a + f * o[j].w;
+            for (int w = 0; w < WPR; ++w) M = fmaxf(M, sml[row * WPR + w].x);
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) {
+                const float f = ex2_approx(sml[row * WPR + w].x - M);
+                total += f * sml[row * WPR + w].y;
+                out += f * so[row * WPR + w][dim];
+            }
+            kv8_store<ROWS, PAIR>(p, seq, b, i, h, r0 + row, dim, out, total, M);
         }
+        __syncthreads();
     }
-    reinterpret_cast<float4*>(so[warp])[lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    if (lane == 0) sml[warp] = make_float2(m, sum);
-    __syncthreads();
-    if (tid >= 128) return;
-    float M = kNoKey, total = 0.f, out = 0.f;
-#pragma unroll
-    for (int w = 0; w < kCombineWarps; ++w) M = fmaxf(M, sml[w].x);
-#pragma unroll
-    for (int w = 0; w < kCombineWarps; ++w) {
-        const float f = ex2_approx(sml[w].x - M);
-        total += f * sml[w].y;
-        out += f * so[w][tid];
-    }
-    kv8_store<ROWS, PAIR>(p, seq, b, hg, u, r, tid, out, total, M);
 }
 
 }  // namespace gqa

@@ -60,7 +60,7 @@ constexpr int kKv8MaxCtas = 480;
 struct Kv8Plan {
     int rows, groups, units;
     long long items;
-    size_t off_ml, off_o, bytes;  // workspace: item starts, partial sums, partial outputs
+    size_t off_ml, off_o, bytes;  // workspace: cut items, partial sums, partial outputs
 };
 Kv8Plan kv8_plan(int B, int Sq, int Hq, int Hkv, int D) {
     Kv8Plan pl;
@@ -72,7 +72,7 @@ Kv8Plan kv8_plan(int B, int Sq, int Hq, int Hkv, int D) {
     pl.units = int((sub * heads + pl.rows - 1) / pl.rows);
     pl.items = (long long)B * pl.groups * pl.units;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    pl.off_ml = up(size_t(pl.items) * 8);
+    pl.off_ml = up(size_t(kKv8MaxCtas) * 16);
     pl.off_o = pl.off_ml + up(size_t(kKv8MaxCtas) * 2 * pl.rows * 8);
     pl.bytes = pl.off_o + size_t(kKv8MaxCtas) * 2 * pl.rows * 128 * 4;
     return pl;
@@ -227,7 +227,9 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
         !aligned(workspace, 16))
         return GQA_ERR_ALIGN;
     const Kv8Plan pl = kv8_plan(B, Sq, Hq, Hkv, D);
-    if (pl.items > INT32_MAX) return GQA_ERR_SHAPE;
+    // tiles of 128 keys are numbered with 31 bits
+    if ((double)pl.items * (((long long)max_pages * page_size + 127) / 128) > INT32_MAX)
+        return GQA_ERR_SHAPE;
     if (!workspace || workspace_bytes < pl.bytes) return GQA_ERR_WORKSPACE;
     DeviceInfo* dev = nullptr;
     rc = device_info(&dev);
@@ -242,7 +244,7 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
     p.seqlens_k = seqlens_k;
     p.cu_seqlens_q = cu_seqlens_q;
     char* ws = static_cast<char*>(workspace);
-    p.meta = reinterpret_cast<int2*>(ws);
+    p.cut = reinterpret_cast<int4*>(ws);
     p.part_ml = reinterpret_cast<float2*>(ws + pl.off_ml);
     p.part_o = reinterpret_cast<float*>(ws + pl.off_o);
     p.B = B;
@@ -281,10 +283,8 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
         const int r2 = launch_pdl(gqa::kv8_decode<rows(), pair()>, dim3(grid), C::THREADS,
                                   C::SMEM_BYTES, stream, tk, tv, p);
         if (r2 != GQA_OK) return r2;
-        const dim3 g(rows(), unsigned(std::min<long long>(pl.items, 65535)),
-                     unsigned((pl.items + 65534) / 65535));
-        return launch_pdl(gqa::kv8_combine<rows(), pair()>, g, 32 * gqa::kCombineWarps, 0, stream,
-                          p);
+        return launch_pdl(gqa::kv8_combine<rows(), pair()>, dim3(grid), 32 * gqa::kCombineWarps, 0,
+                          stream, p);
     };
     auto pick = [&](auto pair, int bit) {
         using std::integral_constant;

@@ -33,57 +33,60 @@ class KvTables:
         self.free_end = free_end
 
 
-def _check(device, **tensors):
+# The checks below run before every launch of a few microseconds, so each looks at a tensor
+# as few times as it can and words its refusal only when there is one.
+def _check(dev, dtype, **tensors):
+    """Contiguous tensors of one type on the GPU of index dev."""
     for name, t in tensors.items():
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-        if t.device != device:
-            raise ValueError(f"{name} must be on the same device as the other tensors")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+        if t.get_device() != dev or t.dtype is not dtype or not t.is_contiguous():
+            _refuse(dev, dtype, name, t)
 
 
-def _int32(torch, **tensors):
-    for name, t in tensors.items():
-        if t.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
+def _refuse(dev, dtype, name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the same device as the other tensors")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _call(torch, name, device, *args):
-    """The C entry point on the current stream of `device`, which is made current."""
-    stream = torch.cuda.current_stream(device).cuda_stream
+def _call(torch, name, dev, *args):
+    """The C entry point on the current stream of GPU dev, which is made current."""
     fn = getattr(_capi.load(), name)
-    if device.index == torch.cuda.current_device():
-        rc = fn(*args, stream)
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream)
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     if rc != 0:
         raise GqaError(name, rc)
 
 
 def _pool(torch, k8, v8, k_scale, v_scale):
-    """(num_pages, page_size, scale_block, Hkv, D) of a cache."""
-    codes = (torch.uint8, torch.float8_e4m3fn)
-    if k8.dtype not in codes or v8.dtype not in codes:
+    """(device index, num_pages, page_size, scale_block, Hkv, D) of a cache."""
+    kind, shape, scales = k8.dtype, k8.shape, k_scale.shape
+    if kind is not torch.float8_e4m3fn and kind is not torch.uint8:
         raise ValueError("k8 and v8 must hold e4m3 codes (uint8 or float8_e4m3fn)")
-    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
-        raise ValueError("k_scale and v_scale must be fp32")
-    if k8.dim() != 4 or v8.shape != k8.shape:
+    if len(shape) != 4 or v8.shape != shape:
         raise ValueError("k8 and v8 are [num_pages, page_size, Hkv, D] and alike")
-    pages, page, Hkv, D = k8.shape
-    if k_scale.dim() != 3 or v_scale.shape != k_scale.shape or k_scale.shape[0] != pages or \
-            k_scale.shape[2] != Hkv or k_scale.shape[1] < 1 or page % k_scale.shape[1]:
+    pages, page, Hkv, D = shape
+    if len(scales) != 3 or v_scale.shape != scales or scales[0] != pages or \
+            scales[2] != Hkv or scales[1] < 1 or page % scales[1]:
         raise ValueError("k_scale and v_scale are [num_pages, page_size / scale_block, Hkv]")
-    _check(k8.device, k8=k8, v8=v8, k_scale=k_scale, v_scale=v_scale)
-    return pages, page, page // k_scale.shape[1], Hkv, D
+    dev = k8.get_device()
+    if dev < 0:
+        _refuse(dev, kind, "k8", k8)
+    _check(dev, kind, k8=k8, v8=v8)
+    _check(dev, torch.float32, k_scale=k_scale, v_scale=v_scale)
+    return dev, pages, page, page // scales[1], Hkv, D
 
 
-def _table(torch, block_table, B, device):
-    _check(device, block_table=block_table)
-    _int32(torch, block_table=block_table)
+def _is_table(block_table, B):
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError("block_table must be [B, max_pages]")
+    return block_table.shape[1]
 
 
 def gqa_attn_kv_tables(cached_lens, new_lens, free_pages, block_table, *, page_size: int,
@@ -98,33 +101,33 @@ def gqa_attn_kv_tables(cached_lens, new_lens, free_pages, block_table, *, page_s
     step's free_start."""
     import torch
 
-    device = block_table.device
+    dev, i32 = block_table.get_device(), torch.int32
+    if dev < 0:
+        _refuse(dev, i32, "block_table", block_table)
     if cached_lens.dim() != 1 or new_lens.shape != cached_lens.shape or free_pages.dim() != 1:
         raise ValueError("cached_lens and new_lens are [B], free_pages is [n]")
     B = cached_lens.shape[0]
-    _table(torch, block_table, B, device)
-    _check(device, cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages)
-    _int32(torch, cached_lens=cached_lens, new_lens=new_lens, free_pages=free_pages)
+    max_pages = _is_table(block_table, B)
+    _check(dev, i32, block_table=block_table, cached_lens=cached_lens, new_lens=new_lens,
+           free_pages=free_pages)
     if free_start is not None:
-        _check(device, free_start=free_start)
-        _int32(torch, free_start=free_start)
+        _check(dev, i32, free_start=free_start)
         if free_start.numel() != 1:
             raise ValueError("free_start must hold one number")
     if not 0 <= max_tokens < 2 ** 31:
         raise ValueError("max_tokens must be in [0, 2^31)")
     # one allocation, cut into the five tables
-    buf = torch.empty(max_tokens + 3 * B + 3, dtype=torch.int32, device=device)
-    t = KvTables(*buf.split([max_tokens, B, B + 1, B + 1, 1]))
-    p = buf.data_ptr()
-    at = [p, p + 4 * max_tokens]
-    at += [at[1] + 4 * B]
-    at += [at[2] + 4 * (B + 1)]
-    at += [at[3] + 4 * (B + 1)]
-    _call(torch, "gqa_attn_kv_tables", device, cached_lens.data_ptr(), new_lens.data_ptr(),
+    sizes = (max_tokens, B, B + 1, B + 1, 1)
+    buf = block_table.new_empty(sum(sizes))
+    p, at = buf.data_ptr(), []
+    for n in sizes:
+        at.append(p)
+        p += 4 * n
+    _call(torch, "gqa_attn_kv_tables", dev, cached_lens.data_ptr(), new_lens.data_ptr(),
           free_pages.data_ptr(), None if free_start is None else free_start.data_ptr(),
-          block_table.data_ptr(), *at, B, free_pages.shape[0], block_table.shape[1],
-          page_size, max_tokens)
-    return t
+          block_table.data_ptr(), *at, B, free_pages.shape[0], max_pages, page_size,
+          max_tokens)
+    return KvTables(*buf.split_with_sizes(sizes))
 
 
 def gqa_attn_kv8_append(k, v, slot_map, k8, v8, k_scale, v_scale) -> None:
@@ -135,26 +138,26 @@ def gqa_attn_kv8_append(k, v, slot_map, k8, v8, k_scale, v_scale) -> None:
     leave out.  Codes and scales of every scale block that receives tokens are updated."""
     import torch
 
-    pages, page, block, Hkv, D = _pool(torch, k8, v8, k_scale, v_scale)
+    dev, pages, page, block, Hkv, D = _pool(torch, k8, v8, k_scale, v_scale)
     if k.dim() != 3 or v.shape != k.shape or k.shape[1:] != (Hkv, D):
         raise ValueError("k and v are [T, Hkv, D], with the cache's heads")
-    T = k.shape[0]
+    T, row = k.shape[0], Hkv * D
     if slot_map.shape != (T,):
         raise ValueError("slot_map must be [T]")
+    strides = []
     for name, t in (("k", k), ("v", v)):
-        if not t.is_cuda or t.device != k8.device:
+        if t.get_device() != dev:
             raise ValueError(f"{name} must be a CUDA tensor on the cache's device")
-        if t.dtype != torch.bfloat16:
+        if t.dtype is not torch.bfloat16:
             raise ValueError(f"{name} must be bf16")
-        if t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D):
+        s0, s1, s2 = t.stride()
+        if s2 != 1 or (Hkv > 1 and s1 != D):
             raise ValueError(f"the heads of a token of {name} must be contiguous")
-    _check(k8.device, slot_map=slot_map)
-    _int32(torch, slot_map=slot_map)
-    row = Hkv * D  # of one token alone a view's stride says nothing
-    _call(torch, "gqa_attn_kv8_append", k8.device, k.data_ptr(), v.data_ptr(),
-          slot_map.data_ptr(), k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
-          v_scale.data_ptr(), T, Hkv, D, k.stride(0) if T > 1 else row,
-          v.stride(0) if T > 1 else row, pages, page, block)
+        strides.append(s0 if T > 1 else row)  # of one token alone it says nothing
+    _check(dev, torch.int32, slot_map=slot_map)
+    _call(torch, "gqa_attn_kv8_append", dev, k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
+          k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), T, Hkv, D,
+          strides[0], strides[1], pages, page, block)
 
 
 def gqa_attn_kv8_gather(k8, v8, k_scale, v_scale, block_table, cu_seqlens_k, *, total: int,
@@ -164,30 +167,31 @@ def gqa_attn_kv8_gather(k8, v8, k_scale, v_scale, block_table, cu_seqlens_k, *, 
     GPU; total: its last entry, or more (rows past it stay as they are)."""
     import torch
 
-    pages, page, block, Hkv, D = _pool(torch, k8, v8, k_scale, v_scale)
-    device = k8.device
+    dev, pages, page, block, Hkv, D = _pool(torch, k8, v8, k_scale, v_scale)
     if cu_seqlens_k.dim() != 1 or cu_seqlens_k.shape[0] < 1:
         raise ValueError("cu_seqlens_k must be [B + 1]")
     B = cu_seqlens_k.shape[0] - 1
-    _table(torch, block_table, B, device)
-    _check(device, cu_seqlens_k=cu_seqlens_k)
-    _int32(torch, cu_seqlens_k=cu_seqlens_k)
+    max_pages = _is_table(block_table, B)
+    _check(dev, torch.int32, block_table=block_table, cu_seqlens_k=cu_seqlens_k)
     if not 0 <= total < 2 ** 31:
         raise ValueError("total must be in [0, 2^31)")
-    out = []
+    bf16, shape, out = torch.bfloat16, (total, Hkv, D), []
     for name, t in (("k", k), ("v", v)):
         if t is None:
-            t = torch.empty((total, Hkv, D), dtype=torch.bfloat16, device=device)
+            t = torch.empty(total, Hkv, D, dtype=bf16, device=k8.device)
         else:
-            _check(device, **{name: t})
-            if t.dtype != torch.bfloat16 or t.shape != (total, Hkv, D):
-                raise ValueError(f"{name} must be bf16 [total, Hkv, D]")
+            _check(dev, bf16, **{name: t})
+            if t.shape != shape:
+                raise ValueError(f"{name} must be [total, Hkv, D]")
         out.append(t)
-    _call(torch, "gqa_attn_kv8_gather", device, k8.data_ptr(), v8.data_ptr(),
-          k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
-          cu_seqlens_k.data_ptr(), out[0].data_ptr(), out[1].data_ptr(), B, total, Hkv, D,
-          pages, page, block_table.shape[1], block)
-    return out[0], out[1]
+    k, v = out
+    _call(torch, "gqa_attn_kv8_gather", dev, k8.data_ptr(), v8.data_ptr(), k_scale.data_ptr(),
+          v_scale.data_ptr(), block_table.data_ptr(), cu_seqlens_k.data_ptr(), k.data_ptr(),
+          v.data_ptr(), B, total, Hkv, D, pages, page, max_pages, block)
+    return k, v
+
+
+_ws_bytes = {}  # workspace size of each problem shape seen
 
 
 def gqa_attn_kv8_decode(q, k8, v8, k_scale, v_scale, block_table, seqlens_k, *,
@@ -203,48 +207,51 @@ def gqa_attn_kv8_decode(q, k8, v8, k_scale, v_scale, block_table, seqlens_k, *,
     Returns (out like q, lse fp32 [B, Hq, Sq], or packed [Hq, total_q])."""
     import torch
 
-    pages, page, block, Hkv, D = _pool(torch, k8, v8, k_scale, v_scale)
-    device = k8.device
-    if q.dtype != torch.bfloat16:
-        raise ValueError("q must be bf16")
-    packed = cu_seqlens_q is not None
-    if packed:
-        if q.dim() != 3 or max_seqlen_q is None:
+    dev, pages, page, block, Hkv, D = _pool(torch, k8, v8, k_scale, v_scale)
+    i32 = torch.int32
+    _check(dev, torch.bfloat16, q=q)
+    shape = q.shape
+    if cu_seqlens_q is not None:
+        if len(shape) != 3 or max_seqlen_q is None:
             raise ValueError("packed q is [total_q, Hq, D], with max_seqlen_q")
         if cu_seqlens_q.dim() != 1 or cu_seqlens_q.shape[0] < 1:
             raise ValueError("cu_seqlens_q must be [B + 1]")
-        _check(device, cu_seqlens_q=cu_seqlens_q)
-        _int32(torch, cu_seqlens_q=cu_seqlens_q)
-        B, Sq, total_q, Hq = cu_seqlens_q.shape[0] - 1, int(max_seqlen_q), q.shape[0], q.shape[1]
+        _check(dev, i32, cu_seqlens_q=cu_seqlens_q)
+        B, Sq, total_q, Hq = cu_seqlens_q.shape[0] - 1, int(max_seqlen_q), shape[0], shape[1]
         lse_shape = (Hq, total_q)
     else:
-        if q.dim() != 4:
+        if len(shape) != 4:
             raise ValueError("q is [B, Sq, Hq, D]")
-        B, Sq, Hq, _ = q.shape
+        B, Sq, Hq, _ = shape
         total_q = B * Sq
         lse_shape = (B, Hq, Sq)
-    if q.shape[-1] != D:
+    if shape[-1] != D:
         raise ValueError("q's head dimension must be the cache's")
-    _check(device, q=q, seqlens_k=seqlens_k)
-    _table(torch, block_table, B, device)
-    _int32(torch, seqlens_k=seqlens_k)
+    max_pages = _is_table(block_table, B)
+    _check(dev, i32, block_table=block_table, seqlens_k=seqlens_k)
     if seqlens_k.shape != (B,):
         raise ValueError("seqlens_k must be [B]")
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _check(dev, torch.bfloat16, out=out)
+        if out.shape != shape:
+            raise ValueError("out must be shaped like q")
     if lse is None:
-        lse = torch.empty(lse_shape, dtype=torch.float32, device=device)
-    _check(device, out=out, lse=lse)
-    if out.shape != q.shape or out.dtype != q.dtype or lse.shape != lse_shape or \
-            lse.dtype != torch.float32:
-        raise ValueError(f"out must be like q and lse fp32 {lse_shape}")
-    need = _capi.load().gqa_attn_kv8_decode_workspace_bytes(B, Sq, Hq, Hkv, D)
-    ws = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _call(torch, "gqa_attn_kv8_decode", device, q.data_ptr(), k8.data_ptr(), v8.data_ptr(),
+        lse = k_scale.new_empty(lse_shape)
+    else:
+        _check(dev, torch.float32, lse=lse)
+        if lse.shape != lse_shape:
+            raise ValueError(f"lse must be {lse_shape}")
+    key = (B, Sq, Hq, Hkv, D)
+    need = _ws_bytes.get(key)
+    if need is None:
+        need = _ws_bytes[key] = _capi.load().gqa_attn_kv8_decode_workspace_bytes(*key)
+    ws = k_scale.new_empty(need // 4)  # of this call alone (the size is a multiple of 16)
+    _call(torch, "gqa_attn_kv8_decode", dev, q.data_ptr(), k8.data_ptr(), v8.data_ptr(),
           k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seqlens_k.data_ptr(),
-          cu_seqlens_q.data_ptr() if packed else None, out.data_ptr(), lse.data_ptr(),
-          ws.data_ptr() if need else None, need, B, Sq, total_q, Hq, Hkv, D, pages, page,
-          block_table.shape[1], block,
-          1.0 / math.sqrt(D) if scale is None else float(scale),
+          None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(), out.data_ptr(),
+          lse.data_ptr(), ws.data_ptr(), need, B, Sq, total_q, Hq, Hkv, D, pages, page,
+          max_pages, block, 1.0 / math.sqrt(D) if scale is None else float(scale),
           min(int(window), 2 ** 31 - 1))
     return out, lse
