@@ -139,10 +139,18 @@ __device__ __forceinline__ Kv8Keys kv8_keys(const Kv8DecodeParams& p, const Kv8S
     return k;
 }
 
-// Tiles are numbered with 31 bits (the host refuses more).  `tiles` of them go to `teams`
-// teams, at most as many: team t starts at floor(tiles * t / teams).
-__device__ __forceinline__ int kv8_range_start(int tiles, int team, int teams) {
-    const int each = tiles / teams, rest = tiles - each * teams;
+// What a CTA's range is measured in: an item with n > 0 tiles counts n + kItemStart, its
+// first kItemStart units standing for its start.  Beginning another item (its q, the first
+// tile's two passes, the last one's results) takes a CTA 4 to 6 us, a tile about 1.3; with
+// equal numbers of tiles the CTAs with more items were that much behind.  Measured at 0 / 2 /
+// 3 / 4: window batch of 32 (D 64) 40.8 / 36.3 / 36.1 / 35.4 us, 4 drafted tokens for 8
+// 41.6 / 40.4 / 38.9 / 38.3, ragged batch of 64 98.3 / 97.6 / 96.9 / 97.7.
+constexpr int kItemStart = 4;
+__device__ __forceinline__ int kv8_cost(int tiles) { return tiles > 0 ? tiles + kItemStart : 0; }
+// Units are numbered with 31 bits (the host refuses more).  `units` of them go to `teams`
+// teams, at most as many: team t starts at floor(units * t / teams).
+__device__ __forceinline__ int kv8_range_start(int units, int team, int teams) {
+    const int each = units / teams, rest = units - each * teams;
     return each * team + rest * team / teams;
 }
 
@@ -151,8 +159,8 @@ __device__ __forceinline__ int kv8_range_start(int tiles, int team, int teams) {
 template <int SUB>
 struct Kv8Walk {
     int b, hs, u;        // the item: sequence, set of `width` head groups, row unit
-    int off;             // its tiles already passed
-    int left;            // tiles of this CTA still to come
+    int off;             // its units already passed
+    int left;            // units of this CTA still to come
     int base;            // lane l holds sequence base + l
     Kv8Seq held;
     Kv8Seq seq;
@@ -173,21 +181,21 @@ struct Kv8Walk {
         keys = kv8_keys<SUB>(p, seq, u);
         n = keys.tiles();
     }
-    __device__ __forceinline__ int held_tiles(const Kv8DecodeParams& p) const {
+    __device__ __forceinline__ int held_units(const Kv8DecodeParams& p) const {
         int t = 0;
-        for (int v = 0; v < p.units; ++v) t += kv8_keys<SUB>(p, held, v).tiles();
+        for (int v = 0; v < p.units; ++v) t += kv8_cost(kv8_keys<SUB>(p, held, v).tiles());
         return t * (p.groups / p.width);
     }
-    // Adds up the tiles of one head group (the result) and goes to the first of the range
-    // of team `team` of `teams`; start: that tile's number.
+    // Adds up the units of one head group (the result) and goes to the first of the range
+    // of team `team` of `teams`; start: that unit's number.
     __device__ __forceinline__ int find(const Kv8DecodeParams& p, int team, int& teams,
                                         int& start) {
         const int sets = p.groups / p.width, lane = threadIdx.x & 31;
         hold(p, 0);
-        int t = held_tiles(p), all = t;
+        int t = held_units(p), all = t;
         for (int x = 32; x < p.B; x += 32) {
             hold(p, x);
-            all += held_tiles(p);
+            all += held_units(p);
         }
         all = __reduce_add_sync(0xffffffffu, all);
         teams = max(min(all, p.teams), 1);
@@ -197,7 +205,7 @@ struct Kv8Walk {
         left = kv8_range_start(all, team + 1, teams) - start;
         if (p.B > 32) {
             hold(p, 0);
-            t = held_tiles(p);
+            t = held_units(p);
         }
         off = start;
         hs = u = 0;
@@ -218,7 +226,7 @@ struct Kv8Walk {
             }
             off -= __shfl_sync(0xffffffffu, inc, 31);
             hold(p, base + 32);
-            t = held_tiles(p);
+            t = held_units(p);
         }
         if (sets > 1) {
             t /= sets;
@@ -226,14 +234,19 @@ struct Kv8Walk {
             off -= hs * t;
         }
         load(p);
-        while (off >= n) {
-            off -= n;
+        while (off >= kv8_cost(n)) {
+            off -= kv8_cost(n);
             ++u;
             load(p);
         }
         return all;
     }
-    __device__ __forceinline__ int segment() const { return min(n - off, left); }
+    // units, and tiles [first, first + tiles) of the item, in this CTA's range
+    __device__ __forceinline__ int segment() const { return min(kv8_cost(n) - off, left); }
+    __device__ __forceinline__ int first() const { return max(off - kItemStart, 0); }
+    __device__ __forceinline__ int tiles() const {
+        return max(off + segment() - kItemStart, 0) - first();
+    }
     __device__ __forceinline__ void next(const Kv8DecodeParams& p) {
         left -= segment();
         off = 0;
@@ -318,6 +331,9 @@ __device__ __forceinline__ void tmem_st_rows(uint32_t taddr, int r0, const float
     tmem_st_wait();
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* at) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+}
 // Whether the phase of `bar` with parity `parity` has completed; never waits
 __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
     uint32_t ok;
@@ -475,28 +491,39 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         int segs = 0;
         auto next_batch = [&](Batch& x) {
             if (seg_now.t >= seg_now.t1) {
+                // (an item may be in the range with nothing but its start)
+                while (walk.left > 0 && walk.tiles() == 0) walk.next(p);
                 if (walk.left <= 0) {
                     x.t = x.t1 = 0;
                     x.seg = -1;
                     return;
                 }
                 Kv8Segment g;
-                g.tiles = walk.segment();
-                g.first = walk.keys.first() + walk.off;
+                g.tiles = walk.tiles();
+                g.first = walk.keys.first() + walk.first();
                 g.b = walk.b, g.hg = walk.hs * p.width + member, g.u = walk.u;
                 g.seq = walk.seq, g.keys = walk.keys;
-                const bool starts = walk.off == 0, whole = starts && g.tiles == walk.n;
+                const bool starts = walk.first() == 0, whole = starts && g.tiles == walk.n;
                 g.slot = whole ? -1 : segs == 0 ? 0 : 1;
                 if (starts && !whole && lane == 0) {
                     // for the combine: the item, the teams it is in (the one with its last
                     // tile is where it ends), and this CTA's partial
-                    const int end = range + (total - walk.left) + walk.n;
+                    const int end = range + (total - walk.left) - walk.off + kv8_cost(walk.n);
                     const int parts = int(((long long)end * teams - 1) / all) - team + 1;
                     p.cut[blockIdx.x] = make_int4(g.b, g.hg, g.u, 2 * parts + g.slot);
                 }
                 // (eight slots: at most two segments ahead of the batch that is copied, and
                 // that one's segment waits for the last but one before it)
                 if (lane == 0) segments[segs & 7] = g;
+                for (int r = lane; r < ROWS && segs > 0; r += 32) {  // q is wanted soon
+                    int i, h;
+                    if (kv8_row<ROWS, PAIR>(p, g.seq, g.hg, g.u, r, i, h)) {
+                        const __nv_bfloat16* q =
+                            p.q + (size_t(g.seq.q0 + i) * p.Hq + h) * (PAIR ? 64 : 128);
+                        prefetch_l2(q);
+                        if (!PAIR) prefetch_l2(q + 64);
+                    }
+                }
                 seg_now = {g.first, g.first + g.tiles, segs++, g.keys.lo, g.keys.hi, g.b, g.hg};
                 walk.next(p);
             }
@@ -971,8 +998,6 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 continue;
             }
             more = stage_q(seg + 1);
-            // the combine may start when every CTA has come this far, and not before: its
-            // CTAs beside these ones, waiting, cost up to a sixth of the rate
             if (!more) griddep_launch_dependents();
             wait_o(c - 1);
             tc_fence_after();

@@ -227,8 +227,9 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
         !aligned(workspace, 16))
         return GQA_ERR_ALIGN;
     const Kv8Plan pl = kv8_plan(B, Sq, Hq, Hkv, D);
-    // tiles of 128 keys are numbered with 31 bits
-    if ((double)pl.items * (((long long)max_pages * page_size + 127) / 128) > INT32_MAX)
+    // tiles of 128 keys, and items' starts, are numbered with 31 bits
+    if ((double)pl.items * (((long long)max_pages * page_size + 127) / 128 + gqa::kItemStart) >
+        INT32_MAX)
         return GQA_ERR_SHAPE;
     if (!workspace || workspace_bytes < pl.bytes) return GQA_ERR_WORKSPACE;
     DeviceInfo* dev = nullptr;
