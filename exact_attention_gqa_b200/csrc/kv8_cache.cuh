@@ -164,6 +164,7 @@ struct Kv8AppendParams {
     const int* slot_map;  // [T]
     int T, Hkv, sb_shift;
     int slots;  // num_pages * page_size
+    int wide;   // warps that share a long run (a power of two, 8 at most)
 };
 
 // The smallest power of two s, at least 2^-126, with a <= 448 s (448 = 1.75 * 2^8); a is
@@ -208,70 +209,147 @@ __device__ __forceinline__ void decode4(uint32_t c, float (&f)[4]) {
         : "r"(hi));
 }
 
-// One warp for each (token, head) of K or V (blockIdx.y); only the warp of a run's first
-// token works, for the whole run: the following tokens of the same scale block.
+// A run is the tokens of one scale block; its first token is its leader.  blockIdx.x takes
+// the leaders among 32 tokens, and its gridDim.y CTAs share the tasks (leader, K or V, head;
+// heads next to each other, as they are in memory).  A warp reads its rows of a task once,
+// into registers (four 16-byte loads a lane); a run of no more rows than that is one warp's
+// task, and if the 32 tokens hold a longer run, `wide` warps share each task (rows beyond
+// what they hold are read twice).
+// Bound: HBM for prompts (2 bytes in, 1 out an element), latency for a decode step.
+constexpr int kAppendHeld = 4;  // 16-byte loads of a lane
+static_assert((kAppendHeld & (kAppendHeld - 1)) == 0, "`wide` must divide a CTA's warps");
 template <int D>
-__global__ void __launch_bounds__(256) kv8_append(const Kv8AppendParams p) {
+__global__ void __launch_bounds__(256, 4) kv8_append(const Kv8AppendParams p) {
     constexpr int LPR = D / 8;       // lanes of one row, eight elements each
     constexpr int RPW = 32 / LPR;    // rows a warp handles at a time
-    const int lane = threadIdx.x & 31;
-    const long long job = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int t = int(job / p.Hkv), h = int(job - (long long)t * p.Hkv);
+    constexpr int HELD = kAppendHeld;
+    __shared__ float sm_amax[2][8];
+    __shared__ int sm_restart[2][8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t0 = blockIdx.x * 32;
     griddep_wait();
-    if (t >= p.T) return;
-    const int slot = __ldg(p.slot_map + t);
-    if (slot < 0 || slot >= p.slots) {
-        if (lane == 0 && slot != -1) raise_device_error(kDevBadKvIndex);
-        return;
-    }
-    const int blk = slot >> p.sb_shift;
-    auto mine = [&](int i) {  // token i belongs to this block
-        const int s = __ldg(p.slot_map + i);
-        return s >= 0 && s < p.slots && (s >> p.sb_shift) == blk;
-    };
-    if (t > 0 && mine(t - 1)) return;
-    int n = 0;
-    for (bool more = true; more;) {
-        const int i = t + n + lane;
-        const uint32_t in = __ballot_sync(0xffffffffu, i < p.T && mine(i));
-        more = in == 0xffffffffu;
-        n += more ? 32 : __ffs(~in) - 1;
-    }
-    const Kv8AppendParams::Side& io = blockIdx.y == 0 ? p.k : p.v;
     const int sb = 1 << p.sb_shift;
-    const int r = lane / LPR, c = lane % LPR;
-    const __nv_bfloat16* x = io.x + (long long)t * io.stride + h * D + c * 8;
-    auto load = [&](int i) {
-        return __ldg(reinterpret_cast<const uint4*>(x + (long long)i * io.stride));
+    auto block_of = [&](int t) {  // token t's scale block, -1: none
+        if (t < 0 || t >= p.T) return -1;
+        const int s = __ldg(p.slot_map + t);
+        return s >= 0 && s < p.slots ? s >> p.sb_shift : -1;
     };
-    float a = 0.f;
-    bool restart = false;
-    for (int i = r; i < n; i += RPW) {
-        a = amax8(load(i), a);
-        restart |= (__ldg(p.slot_map + t + i) & (sb - 1)) == 0;
+    const int mine = block_of(t0 + lane), after = block_of(t0 + 32 + lane);
+    int before = block_of(t0 - 1);
+    if (blockIdx.y == 0 && warp == 0 && mine < 0 && t0 + lane < p.T &&
+        __ldg(p.slot_map + t0 + lane) != -1)
+        raise_device_error(kDevBadKvIndex);
+    const int left = __shfl_up_sync(0xffffffffu, mine, 1);
+    if (lane > 0) before = left;
+    const uint32_t starts = __ballot_sync(0xffffffffu, mine != before);
+    const uint32_t leaders = __ballot_sync(0xffffffffu, mine >= 0 && mine != before);
+    if (leaders == 0) return;
+    // the runs' lengths: up to the next start, the last one's maybe beyond these 32
+    const uint32_t later = lane < 31 ? starts >> (lane + 1) << (lane + 1) : 0u;
+    int my_n = (leaders >> lane & 1) ? (later ? __ffs(later) - 1 : 32) - lane : 0;
+    const int last = 31 - __clz(leaders);
+    if (__shfl_sync(0xffffffffu, later, last) == 0) {
+        const int blk = __shfl_sync(0xffffffffu, mine, last);
+        int n = 0, next = after;
+        while (true) {
+            const uint32_t in = __ballot_sync(0xffffffffu, next == blk);
+            if (in != 0xffffffffu) {
+                n += __ffs(~in) - 1;
+                break;
+            }
+            n += 32;
+            next = block_of(t0 + 32 + n + lane);
+        }
+        if (lane == last) my_n += n;
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-    restart = __any_sync(0xffffffffu, restart);
-    float s = pow2_scale(fminf(a, kBf16Max));  // infinity: the largest finite value
-    float* scale = io.scale + (size_t(blk) * p.Hkv + h);
-    uint8_t* base = io.codes + (size_t(blk) << p.sb_shift) * p.Hkv * D + h * D + c * 8;
+    const int longest = __reduce_max_sync(0xffffffffu, my_n);
+    const int team = longest > HELD * RPW ? p.wide : 1;  // warps of a task
+    const int teams = 8 / team, my_team = warp / team, wi = warp - my_team * team;
+    auto sync = [&]() {
+        if (team > 1)
+            asm volatile("bar.sync %0, %1;" ::"r"(my_team + 1), "r"(team * 32) : "memory");
+    };
+    const int tasks = __popc(leaders) * 2 * p.Hkv;
+    const int r = wi * RPW + lane / LPR, c = lane % LPR, step = team * RPW;
     const size_t row = size_t(p.Hkv) * D;
-    if (!restart) {
+    int parity = 0;
+    struct Task {
+        const __nv_bfloat16* x;  // this lane's elements of the run's first row
+        long long stride;
+        float* scale;
+        uint8_t* codes;          // and of the block's first
+        int t, n;                // the run
+        float s0;                // the block's scale before
+        uint4 held[HELD];
+        int at[HELD];            // the rows' positions in the block
+    };
+    auto load = [&](const Task& k, int i) {
+        return __ldg(reinterpret_cast<const uint4*>(k.x + (long long)i * k.stride));
+    };
+    auto fetch = [&](Task& k, int task) {
+        const int which = task / p.Hkv, h = task - which * p.Hkv;
+        const Kv8AppendParams::Side& io = which & 1 ? p.v : p.k;
+        const int l = __fns(leaders, 0, (which >> 1) + 1);  // the leader's lane
+        const int blk = __shfl_sync(0xffffffffu, mine, l);
+        k.n = __shfl_sync(0xffffffffu, my_n, l);
+        k.t = t0 + l;
+        k.stride = io.stride;
+        k.x = io.x + (long long)k.t * io.stride + h * D + c * 8;
+        k.scale = io.scale + (size_t(blk) * p.Hkv + h);
+        k.codes = io.codes + (size_t(blk) << p.sb_shift) * row + h * D + c * 8;
+        k.s0 = *k.scale;
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) {
+            const int i = r + j * step;
+            k.held[j] = make_uint4(0u, 0u, 0u, 0u);
+            k.at[j] = 1;
+            if (i < k.n) {
+                k.held[j] = load(k, i);
+                k.at[j] = __ldg(p.slot_map + k.t + i);
+            }
+        }
+    };
+    auto finish = [&](const Task& k) {
+        float a = 0.f;
+        bool restart = false;
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) {
+            a = amax8(k.held[j], a);
+            restart |= (k.at[j] & (sb - 1)) == 0;
+        }
+        for (int i = r + HELD * step; i < k.n; i += step) {
+            a = amax8(load(k, i), a);
+            restart |= (__ldg(p.slot_map + k.t + i) & (sb - 1)) == 0;
+        }
+        a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));  // (a >= 0)
+        restart = __any_sync(0xffffffffu, restart);
+        if (team > 1) {
+            if (lane == 0) {
+                sm_amax[parity][warp] = a;
+                sm_restart[parity][warp] = restart;
+            }
+            // (every warp has read the old scale before the first writes the new one)
+            asm volatile("bar.sync %0, %1;" ::"r"(my_team + 1), "r"(team * 32) : "memory");
+            for (int w = my_team * team; w < (my_team + 1) * team; ++w) {
+                a = fmaxf(a, sm_amax[parity][w]);
+                restart |= sm_restart[parity][w] != 0;
+            }
+            parity ^= 1;
+        }
+        float s = pow2_scale(fminf(a, kBf16Max));  // infinity: the largest finite value
         // a scale that no append wrote (not finite, not positive) holds nothing to keep
-        const float s0 = *scale;
-        if (s0 > 0.f && s0 < INFINITY) {
-            const uint32_t u = __float_as_uint(s0);
-            const float up = (u & 0x7fffffu) ? __uint_as_float(((u >> 23) + 1) << 23) : s0;
+        if (!restart && k.s0 > 0.f && k.s0 < INFINITY) {
+            const uint32_t u = __float_as_uint(k.s0);
+            const float up = (u & 0x7fffffu) ? __uint_as_float(((u >> 23) + 1) << 23) : k.s0;
             s = fmaxf(s, fminf(fmaxf(up, 1.1754943508222875e-38f), 1.7014118346046923e38f));
-            if (s != s0) {
-                const float f = s0 / s;
-                for (int i = r; i < sb; i += RPW) {
+            if (s != k.s0) {
+                const float f = k.s0 / s;
+                for (int i = r; i < sb; i += step) {
                     bool now = false;  // written by this call
-                    for (int j = 0; j < n; ++j)
-                        now |= (__ldg(p.slot_map + t + j) & (sb - 1)) == i;
+                    for (int j = 0; j < k.n; ++j)
+                        now |= (__ldg(p.slot_map + k.t + j) & (sb - 1)) == i;
                     if (now) continue;
-                    uint2* d = reinterpret_cast<uint2*>(base + i * row);
+                    uint2* d = reinterpret_cast<uint2*>(k.codes + i * row);
                     const uint2 o = *d;
                     float y[4], z[4];
                     decode4(o.x, y);
@@ -281,13 +359,22 @@ __global__ void __launch_bounds__(256) kv8_append(const Kv8AppendParams p) {
                 }
             }
         }
-    }
-    __syncwarp();  // every lane has read the old scale
-    if (lane == 0) *scale = s;
-    const float inv = 1.f / s;
-    for (int i = r; i < n; i += RPW) {
-        const int off = __ldg(p.slot_map + t + i) & (sb - 1);
-        *reinterpret_cast<uint2*>(base + off * row) = encode8(load(i), inv);
+        if (lane == 0 && wi == 0) *k.scale = s;
+        const float inv = 1.f / s;
+#pragma unroll
+        for (int j = 0; j < HELD; ++j)
+            if (r + j * step < k.n)
+                *reinterpret_cast<uint2*>(k.codes + (k.at[j] & (sb - 1)) * row) =
+                    encode8(k.held[j], inv);
+        for (int i = r + HELD * step; i < k.n; i += step) {
+            const int off = __ldg(p.slot_map + k.t + i) & (sb - 1);
+            *reinterpret_cast<uint2*>(k.codes + off * row) = encode8(load(k, i), inv);
+        }
+    };
+    for (int task = blockIdx.y * teams + my_team; task < tasks; task += gridDim.y * teams) {
+        Task k;
+        fetch(k, task);
+        finish(k);
     }
 }
 
@@ -305,18 +392,36 @@ struct Kv8GatherParams {
 };
 
 // kGatherRows packed rows of K or V (blockIdx.y) per CTA: their source rows are looked up
-// once, then every thread converts eight elements at a time.
-constexpr int kGatherRows = 16;
+// once, then every thread converts 8 elements at a time (so that a warp's stores are whole
+// 512-byte pieces), eight loads in flight.
+// Bound: HBM (1 byte in, 2 out an element).
+constexpr int kGatherRows = 32;
 __global__ void __launch_bounds__(256) kv8_gather(const Kv8GatherParams p) {
+    static_assert(kGatherRows % 32 == 0, "whole warps look the rows up");
     __shared__ int src[kGatherRows];  // row of the pool, -1: none
     const int row0 = blockIdx.x * kGatherRows;
     griddep_wait();
     if (threadIdx.x < kGatherRows) {
         const int t = row0 + threadIdx.x;
         int s = -1;
-        if (t < p.total && t < __ldg(p.cu_seqlens_k + p.B)) {
-            const int b = owner_of(p.cu_seqlens_k, p.B, t);
-            const int pos = t - __ldg(p.cu_seqlens_k + b);
+        int b = 0, first = 0, end;
+        if (p.B <= 32) {  // the lanes hold the prefix sums: one load, five steps of registers
+            const int lane = threadIdx.x & 31;
+            const int cu = __ldg(p.cu_seqlens_k + min(lane, p.B - 1));
+            end = __ldg(p.cu_seqlens_k + p.B);
+#pragma unroll
+            for (int step = 16; step > 0; step >>= 1) {
+                const int at = __shfl_sync(0xffffffffu, cu, min(b + step, 31));
+                if (b + step < p.B && at <= t) b += step;
+            }
+            first = __shfl_sync(0xffffffffu, cu, b);
+        } else {
+            end = __ldg(p.cu_seqlens_k + p.B);
+            b = owner_of(p.cu_seqlens_k, p.B, t);
+            first = __ldg(p.cu_seqlens_k + b);
+        }
+        if (t < p.total && t < end) {
+            const int pos = t - first;
             const int lp = pos >> p.page_shift;
             int page = (pos >= 0 && lp < p.max_pages)
                            ? __ldg(p.block_table + size_t(b) * p.max_pages + lp)
@@ -331,21 +436,35 @@ __global__ void __launch_bounds__(256) kv8_gather(const Kv8GatherParams p) {
     }
     __syncthreads();
     const Kv8GatherParams::Side& io = blockIdx.y == 0 ? p.k : p.v;
-    const int chunks = p.Hkv * p.D / 8;  // of one row
-    for (int e = threadIdx.x; e < kGatherRows * chunks; e += blockDim.x) {
-        const int i = e / chunks, c = e - i * chunks;
-        const int s = src[i];
-        if (s < 0) continue;
-        const int h = c * 8 / p.D;
-        const float f = __ldg(io.scale + size_t(s >> p.sb_shift) * p.Hkv + h);
-        const uint2 o =
-            __ldg(reinterpret_cast<const uint2*>(io.codes + size_t(s) * chunks * 8) + c);
-        float y[4], z[4];
-        decode4(o.x, y);
-        decode4(o.y, z);
-        reinterpret_cast<uint4*>(io.out + size_t(row0 + i) * chunks * 8)[c] = make_uint4(
-            pack_bf16x2(y[0] * f, y[1] * f), pack_bf16x2(y[2] * f, y[3] * f),
-            pack_bf16x2(z[0] * f, z[1] * f), pack_bf16x2(z[2] * f, z[3] * f));
+    const uint32_t chunks = uint32_t(p.Hkv) * p.D / 8;  // of one row
+    const uint32_t end = kGatherRows * chunks;
+    const int per_head = p.D == 128 ? 4 : 3;  // log2 of a head's chunks
+    for (uint32_t e0 = threadIdx.x; e0 < end; e0 += 8 * 256) {
+        uint2 o[8];
+        float f[8];
+        uint4* out[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t e = e0 + j * 256, i = e / chunks, c = e - i * chunks;
+            const int s = e < end ? src[i] : -1;
+            out[j] = nullptr;
+            if (s >= 0) {
+                o[j] = __ldg(reinterpret_cast<const uint2*>(io.codes + size_t(s) * chunks * 8) + c);
+                f[j] = __ldg(io.scale + size_t(s >> p.sb_shift) * p.Hkv + (c >> per_head));
+                out[j] = reinterpret_cast<uint4*>(io.out + size_t(row0 + i) * chunks * 8) + c;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!out[j]) continue;
+            float x[4], y[4];
+            decode4(o[j].x, x);
+            decode4(o[j].y, y);
+            __stcs(out[j], make_uint4(pack_bf16x2(x[0] * f[j], x[1] * f[j]),
+                                      pack_bf16x2(x[2] * f[j], x[3] * f[j]),
+                                      pack_bf16x2(y[0] * f[j], y[1] * f[j]),
+                                      pack_bf16x2(y[2] * f[j], y[3] * f[j])));
+        }
     }
 }
 

@@ -78,6 +78,7 @@ Kv8Plan kv8_plan(int B, int Sq, int Hq, int Hkv, int D) {
     return pl;
 }
 
+constexpr int kAppendShare = 4;
 constexpr int kTablesMaxRequests = 16384;  // two ints of shared memory each
 
 }  // namespace
@@ -147,8 +148,6 @@ int gqa_attn_kv8_append(const void* k, const void* v, const int* slot_map, void*
         !aligned(slot_map, 4) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
         k_stride % 8 != 0 || v_stride % 8 != 0)
         return GQA_ERR_ALIGN;
-    const long long grid = ((long long)T * Hkv + 7) / 8;
-    if (grid > INT32_MAX) return GQA_ERR_SHAPE;
     DeviceInfo* dev = nullptr;
     const int drc = device_info(&dev);
     if (drc != GQA_OK) return drc;
@@ -160,7 +159,17 @@ int gqa_attn_kv8_append(const void* k, const void* v, const int* slot_map, void*
     p.Hkv = Hkv;
     p.sb_shift = log2_exact(scale_block);
     p.slots = num_pages * page_size;
-    const dim3 g(static_cast<unsigned>(grid), 2);
+    const int held = gqa::kAppendHeld * 256 / D;  // rows
+    p.wide = std::max(1, std::min(8, scale_block / held));
+    // CTAs for each 32 tokens: as many as run at a time (four an SM), up to a warp for each
+    // (token, K or V, head); for prompts kAppendShare, each with a few tasks then.  2048
+    // single tokens: 18.8 us (22.1 with eight times as many CTAs), prompts of 4 x 8192
+    // tokens: 55.5 us (58.6 with 8 CTAs for each 32).
+    const int windows = (T + 31) / 32;
+    const int all = (32 * 2 * Hkv + 7) / 8;
+    const int share =
+        std::max(std::min(kAppendShare, all), std::min(all, 4 * dev->sms / windows));
+    const dim3 g(windows, share);
     return launch_pdl(D == 128 ? gqa::kv8_append<128> : gqa::kv8_append<64>, g, 256, 0, stream, p);
 }
 
