@@ -104,7 +104,10 @@ int gqa_attn_kv_tables(const int* cached_lens, const int* new_lens, const int* f
                          static_cast<const int*>(cu_seqlens_k),
                          static_cast<const int*>(free_end)})
         if (!aligned(x, 4)) return GQA_ERR_ALIGN;
-    if (free_start == free_end) return GQA_ERR_SHAPE;  // read by every CTA, written by one
+    // inputs that every CTA reads and outputs that one writes
+    for (const int* in : {cached_lens, new_lens, free_pages, free_start})
+        for (const int* out : {slot_map, seqlens_k, cu_seqlens_q, cu_seqlens_k, free_end})
+            if (in && in == out) return GQA_ERR_SHAPE;
     DeviceInfo* dev = nullptr;
     int rc = device_info(&dev);
     if (rc != GQA_OK) return rc;
@@ -222,9 +225,11 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
                         float scale, int window, cudaStream_t stream) {
     int rc = check_pool(num_pages, page_size, scale_block, Hkv, D);
     if (rc != GQA_OK) return rc;
-    if (B < 0 || Sq < 0 || total_q < 0 || window < 0 || max_pages < 1 ||
-        (long long)max_pages * page_size > INT32_MAX)
+    const long long cap = (long long)max_pages * page_size;  // keys a sequence can have
+    if (B < 0 || Sq < 0 || Sq > 65535 || total_q < 0 || window < 0 || max_pages < 1 ||
+        cap > (1 << 30))
         return GQA_ERR_SHAPE;
+    if (window >= cap) window = 0;  // every key
     rc = check_shape(B, Hq, Hkv, Sq, 0, D, scale, 1, -1, cu_seqlens_q != nullptr, false);
     if (rc != GQA_OK) return rc;
     if (B == 0 || Sq == 0 || (cu_seqlens_q && total_q == 0)) return GQA_OK;
@@ -237,8 +242,7 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
         return GQA_ERR_ALIGN;
     const Kv8Plan pl = kv8_plan(B, Sq, Hq, Hkv, D);
     // tiles of 128 keys, and items' starts, are numbered with 31 bits
-    if ((double)pl.items * (((long long)max_pages * page_size + 127) / 128 + gqa::kItemStart) >
-        INT32_MAX)
+    if ((double)pl.items * ((cap + 127) / 128 + gqa::kItemStart) > INT32_MAX)
         return GQA_ERR_SHAPE;
     if (!workspace || workspace_bytes < pl.bytes) return GQA_ERR_WORKSPACE;
     DeviceInfo* dev = nullptr;
@@ -285,8 +289,7 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
         // tile of one head group at most
         p.width = std::min(pl.groups, 16);
         while (pl.groups % p.width) --p.width;
-        const long long tiles = pl.items / p.width *
-                                (((long long)max_pages * page_size + 127) / 128);
+        const long long tiles = pl.items / p.width * ((cap + 127) / 128);
         p.teams = int(std::min<long long>(
             tiles, std::min(C::CTAS_PER_SM * sms, kKv8MaxCtas) / p.width));
         const int grid = p.teams * p.width;

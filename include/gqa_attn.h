@@ -458,8 +458,9 @@ int gqa_attn_decode_fp8(const void* q, const void* k8, const void* v8, float k_s
  *     new_lens and of seqlens_k (at most 2^31 - 1);
  *   slot_map[cu_seqlens_q[b] + i] = slot of position cached + i; -1 from
  *     cu_seqlens_q[B] to max_tokens;
- *   *free_end = *free_start + the pages taken: the next step's free_start (a buffer of
- *     its own: GQA_ERR_SHAPE if it is free_start's).
+ *   *free_end = *free_start + the pages taken: the next step's free_start.
+ * No output may overlap an input (GQA_ERR_SHAPE if one starts where one does): copy
+ * free_end to free_start, and seqlens_k to cached_lens, for the next step.
  * Device error 4: a negative length, one past max_pages * page_size (both are clamped),
  * more tokens than max_tokens (the rest get no slot) or fewer free pages than needed
  * (*free_end > n_free; the entries and slots without a page are -1).  B <= 16384.
@@ -515,8 +516,11 @@ int gqa_attn_kv8_gather(const void* k8, const void* v8, const float* k_scale,
  *   else packed: q, out [total_q, Hq, D], lse [Hq, total_q], n_b = cu_seqlens_q[b + 1] -
  *     cu_seqlens_q[b] <= Sq; rows from cu_seqlens_q[B] to total_q are left as they are
  *     (a range that does not fit raises device error 2 and is left out).
- *   block_table [B, max_pages], seqlens_k [B]: as gqa_attn_decode_paged; only entries of
- *     pages that hold a visible key are read.
+ *   block_table [B, max_pages], seqlens_k [B]: as gqa_attn_decode_paged, max_pages *
+ *     page_size at most 2^30, Sq at most 65535; of a sequence's entries only those of
+ *     pages that hold a visible key are used.
+ * All B sequences together: their row units (rows of up to 32 query heads x positions of a
+ *     KV head, or of two KV heads at D = 64) times max_pages * page_size / 128 below 2^31.
  * Scales: any finite normal positive fp32.  What lies in the pool outside the visible keys is
  * never used, whatever its codes.  workspace: gqa_attn_kv8_decode_workspace_bytes(B, Sq, Hq,
  * Hkv, D) bytes, 16-byte aligned, private to the call until it has run: a parameter and

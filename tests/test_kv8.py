@@ -23,8 +23,8 @@ def lib():
     return _capi.load()
 
 
-def tables(lib, cached=FAKE, new=FAKE, free=FAKE, start=None, bt=FAKE, slots=FAKE, lens=FAKE,
-           cq=FAKE, ck=FAKE, end=odd(64), B=2, n_free=4, max_pages=3, page=64, max_tokens=5):
+def tables(lib, cached=odd(16), new=odd(32), free=odd(48), start=None, bt=odd(80),
+           slots=FAKE, lens=FAKE, cq=FAKE, ck=FAKE, end=odd(64), B=2, n_free=4, max_pages=3, page=64, max_tokens=5):
     return G.STATUS[lib.gqa_attn_kv_tables(cached, new, free, start, bt, slots, lens, cq, ck, end,
                                            B, n_free, max_pages, page, max_tokens, None)]
 
@@ -39,6 +39,7 @@ def tables(lib, cached=FAKE, new=FAKE, free=FAKE, start=None, bt=FAKE, slots=FAK
     (dict(max_tokens=-1), "GQA_ERR_SHAPE"),
     (dict(n_free=-1), "GQA_ERR_SHAPE"),
     (dict(start=odd(64)), "GQA_ERR_SHAPE"),             # free_end's own buffer
+    (dict(cached=odd(128), lens=odd(128)), "GQA_ERR_SHAPE"),
     (dict(cached=None), "GQA_ERR_NULL"),
     (dict(new=None), "GQA_ERR_NULL"),
     (dict(free=None), "GQA_ERR_NULL"),
@@ -124,7 +125,10 @@ def decode(lib, q=FAKE, k8=FAKE, v8=FAKE, ks=FAKE, vs=FAKE, bt=FAKE, sl=FAKE, cu
 @pytest.mark.parametrize("kw,code", BAD_POOLS + [
     (dict(B=-1), "GQA_ERR_SHAPE"),
     (dict(Sq=-1), "GQA_ERR_SHAPE"),
+    (dict(Sq=65536), "GQA_ERR_SHAPE"),
     (dict(window=-1), "GQA_ERR_SHAPE"),
+    (dict(max_pages=(1 << 24) + 1), "GQA_ERR_SHAPE"),   # sequences past 2^30 keys
+    (dict(B=1 << 16, max_pages=1 << 16), "GQA_ERR_SHAPE"),  # tiles past 2^31
     (dict(Hq=7), "GQA_ERR_SHAPE"),
     (dict(max_pages=0), "GQA_ERR_SHAPE"),
     (dict(scale=0.0), "GQA_ERR_SCALE"),
@@ -138,6 +142,8 @@ def decode(lib, q=FAKE, k8=FAKE, v8=FAKE, ks=FAKE, vs=FAKE, bt=FAKE, sl=FAKE, cu
     (dict(lse=odd(2)), "GQA_ERR_ALIGN"),
     (dict(cu=odd(2)), "GQA_ERR_ALIGN"),
     (dict(ws=odd(8)), "GQA_ERR_ALIGN"),
+    (dict(ws=None), "GQA_ERR_WORKSPACE"),
+    (dict(ws_bytes=1000), "GQA_ERR_WORKSPACE"),
 ])
 def test_decode_argument_errors(lib, kw, code):
     assert decode(lib, **kw) == code

@@ -310,6 +310,25 @@ def test_decode(Hq, H, D, page, block):
     run_decode(LENS, Hq, H, D, page, block, seed=Hq + page)
 
 
+@pytest.mark.parametrize("Hq,H,D", [(24, 24, 128), (34, 17, 128), (33, 33, 64), (64, 32, 64),
+                                    (20, 20, 64)])
+def test_decode_head_counts(Hq, H, D):
+    """Head groups that fill teams of 12, 1, 1, 16 and 10 CTAs."""
+    run_decode(LENS, Hq, H, D, 32, 16, seed=Hq)
+
+
+def test_decode_nothing_to_see():
+    run_decode([0, 0, 0], 8, 2, 128, 16, 16, seed=1)
+    run_decode([0, 0, 0], 4, 2, 64, 16, 16, n=3, seed=1)
+    run_decode([2, 0, 1], 8, 2, 128, 16, 16, n=5, seed=1)    # more queries than keys
+
+
+def test_decode_many_sequences_of_any_length():
+    lens = np.random.default_rng(3).integers(0, 400, 77).tolist()
+    run_decode(lens, 4, 2, 64, 16, 16, n=2, seed=5)
+    run_decode(lens, 8, 2, 128, 16, 16, seed=6)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("n,window", [(1, 1), (1, 100), (1, 5000), (2, 0), (3, 17), (5, 128),
                                       (8, 0), (20, 0), (40, 300)])
@@ -378,6 +397,69 @@ def test_decode_reports_bad_lengths_pages_and_query_ranges():
     G.gqa_attn_kv8_decode(q[:, 0].contiguous(), *d, table.to(DEV), i32(lens),
                           cu_seqlens_q=i32([0, 1, 3]), max_seqlen_q=2)
     assert gqa_attn_get_device_error() == 2
+
+
+def test_a_pool_past_four_gigabytes():
+    """Rows, codes and scales whose offsets pass 32 bits: only the last pages are used."""
+    pages, page, block, H, D = 4200, 256, 64, 32, 128       # 4.4 GB each of K and V
+    k8 = torch.empty(pages, page, H, D, dtype=torch.uint8, device=DEV)
+    v8 = torch.empty_like(k8)
+    ks = torch.empty(pages, page // block, H, device=DEV)
+    vs = torch.empty_like(ks)
+    assert k8.numel() > 2 ** 32
+    L = 300
+    table = i32([[pages - 1, pages - 2]])
+    slots = [(pages - 1) * page + i for i in range(page)] + \
+        [(pages - 2) * page + i for i in range(L - page)]
+    k, v = draw_kv(L, H, D, seed=3, spread=1.0)
+    G.gqa_attn_kv8_append(k.to(DEV), v.to(DEV), i32(slots), k8, v8, ks, vs)
+    g = torch.Generator().manual_seed(4)
+    q = (1.5 * torch.randn(1, 1, 2 * H, D, generator=g)).bfloat16()
+    out, lse = G.gqa_attn_kv8_decode(q.to(DEV), k8, v8, ks, vs, table, i32([L]))
+    kg, vg = G.gqa_attn_kv8_gather(k8, v8, ks, vs, table, i32([0, L]), total=L)
+    torch.cuda.synchronize()
+    local = list(range(page, 2 * page)) + list(range(L - page))  # the last page first
+    zc, zs = np.zeros((2 * page, H, D), np.uint8), np.full((2 * page // block, H), math.nan)
+    (kc, ksc), (vc, vsc) = (P.append(x.double().numpy(), local, zc, zs, block) for x in (k, v))
+    kk, vv = P.gather(kc, ksc, [1, 0], L, page, block), P.gather(vc, vsc, [1, 0], L, page, block)
+    assert torch.equal(kg.cpu(), torch.from_numpy(kk).bfloat16())
+    assert torch.equal(vg.cpu(), torch.from_numpy(vv).bfloat16())
+    ref = P.decode(q[0].double().numpy(), kk, vv, 1, D ** -0.5, 0, 2,
+                   P.coarse(vc, vsc, [1, 0], L, page, block))
+    P.check_decode(out[0].float().cpu().numpy(), lse[0].T.cpu().numpy(), ref, D ** -0.5)
+
+
+def test_append_many_single_tokens_and_long_runs_side_by_side():
+    """Windows of 32 tokens that hold single tokens, whole blocks, and both."""
+    H, D, page, block = 3, 64, 256, 256
+    rng = np.random.default_rng(1)
+    slots, pages = [], 0
+    for n in [1] * 40 + [300, 1, 1, 256, 3, 700] + [2] * 20:
+        off = int(rng.integers(0, page)) if n < 10 else 0
+        slots += [pages * page + off % (page - n) + i if n < 10 else pages * page + i
+                  for i in range(n)]
+        pages += -(-n // page)
+    k, v = draw_kv(len(slots), H, D, seed=12)
+    run_append(k, v, slots, page, block, H, D, pages, seed=13)
+
+
+def test_append_then_attend_without_waiting_on_either_side():
+    """Back to back launches that may begin early still see all of what came before."""
+    H, D, page = 8, 128, 64
+    lens = [page * 4] * 16
+    cache = build_cache(lens, page, 16, H, D, seed=50, garbage_rest=False)
+    d = [t.to(DEV) for t in cache]
+    q = torch.randn(16, 1, 32, D, device=DEV).bfloat16()
+    k, v = (x.to(DEV) for x in draw_kv(16 * page, H, D, seed=51, spread=0.5))
+    slots = torch.cat([d[4][:, 3:4] * page + torch.arange(page, device=DEV)], 1)
+    slots = slots.reshape(-1).to(torch.int32)
+    seq, ref = i32(lens), None
+    for _ in range(30):
+        d[0].view(-1, page, H, D)[d[4][:, 3].long()] = 0
+        G.gqa_attn_kv8_append(k, v, slots, *d[:4])
+        out, lse = G.gqa_attn_kv8_decode(q, *d, seq)
+        ref = (out.clone(), lse.clone()) if ref is None else ref
+        assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
 
 
 # ----------------------------------------------------------------- a run of them together
