@@ -53,7 +53,8 @@ struct Kv8DecodeParams {
     const int* cu_seqlens_q;  // [B + 1] or null: Sq queries each
     float* part_o;            // [CTAs, 2, R, 128] fp32 partials of a CTA's cut items
     float2* part_ml;          // [CTAs, 2, R] reference (log2 units) and sum
-    int4* cut;                // [CTAs] the item that starts in a CTA's range and ends in another's
+    int4* cut;                // [CTAs][2] the item that starts in a CTA's range and ends in
+                              // another's, and its sequence
     int B, Sq, total_q, Hq, Hkv, G;
     int groups, units;        // head groups (KV heads, or pairs of them); row units of each
     int width, teams;         // CTAs of a team (divides groups), teams of the grid
@@ -510,7 +511,8 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     // tile is where it ends), and this CTA's partial
                     const int end = range + (total - walk.left) - walk.off + kv8_cost(walk.n);
                     const int parts = int(((long long)end * teams - 1) / all) - team + 1;
-                    p.cut[blockIdx.x] = make_int4(g.b, g.hg, g.u, 2 * parts + g.slot);
+                    p.cut[2 * blockIdx.x] = make_int4(g.b, g.hg, g.u, 2 * parts + g.slot);
+                    p.cut[2 * blockIdx.x + 1] = make_int4(g.seq.q0, g.seq.n, g.seq.len, 0);
                 }
                 // (eight slots: at most two segments ahead of the batch that is copied, and
                 // that one's segment waits for the last but one before it)
@@ -559,7 +561,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         int c = 0, copied[2] = {0, 0};  // tiles; copies of K and of V issued
         bool ok = true;
         Batch now;
-        if (lane == 0) p.cut[blockIdx.x].x = -1;  // unless an item is cut
+        if (lane == 0) p.cut[2 * blockIdx.x].x = -1;  // unless an item is cut
         __syncwarp();
         next_batch(now);
         if (lane == 0 && now.seg == 0) mbar_arrive(seg_ready);
@@ -1055,44 +1057,32 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
 // Joins the partials of the items that several teams shared, and writes the rows of items
 // that no key reaches.  With reference M = max_s m_s (log2 units): sum = sum_s 2^(m_s - M)
 // sum_s, O = sum_s 2^(m_s - M) O_s / sum, L = ln 2 (M + log2 sum).
-// CTA c takes the one item that CTA c of kv8_decode may have begun and not ended, and every
-// gridDim-th item's check for keys.  16 warps: several to a row, or several rows to one; a
-// warp takes four partials at a time, with an online rescaling of its own.
-constexpr int kCombineWarps = 16;
+// blockIdx.x: the one item that this CTA of kv8_decode may have begun and not ended, and
+// every gridDim.x-th item's check for keys; blockIdx.y: four of its rows.  Eight warps, two
+// to a row; a warp takes eight partials at a time, all loads in flight together (what
+// bounds this kernel is latency), with an online rescaling of its own.
+constexpr int kCombineWarps = 8;
+constexpr int kCombineRows = 4;  // of a CTA
 template <int ROWS, bool PAIR>
 __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine(const Kv8DecodeParams p) {
     constexpr int SUB = PAIR ? ROWS / 2 : ROWS;
-    constexpr int WPR = ROWS < kCombineWarps ? kCombineWarps / ROWS : 1;  // warps of a row
-    constexpr int PASS = kCombineWarps / WPR;                             // rows at a time
+    constexpr int CR = kCombineRows, WPR = kCombineWarps / CR;
     __shared__ __align__(16) float so[kCombineWarps][128];
     __shared__ float2 sml[kCombineWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int r0 = blockIdx.y * CR;
     griddep_wait();
-    const int4 cut = p.cut[blockIdx.x];
-    const int items = p.B * p.groups * p.units;
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int bh = item / p.units, u = item - bh * p.units;
-        const int b = bh / p.groups, hg = bh - b * p.groups;
-        const Kv8Seq seq = kv8_seq(p, b);
-        if (kv8_keys<SUB>(p, seq, u).tiles() > 0) continue;
-        for (int x = tid; x < ROWS * 128; x += 32 * kCombineWarps) {
-            int i, h;
-            if (kv8_row<ROWS, PAIR>(p, seq, hg, u, x >> 7, i, h))
-                kv8_store<ROWS, PAIR>(p, seq, b, i, h, x >> 7, x & 127, 0.f, 0.f, kNoKey);
-        }
-    }
-    if (cut.x < 0) return;
-    const int b = cut.x, hg = cut.y, u = cut.z, parts = cut.w >> 1;
-    const Kv8Seq seq = kv8_seq(p, b);
-#pragma unroll 1
-    for (int r0 = 0; r0 < ROWS; r0 += PASS) {
+    const int4 cut = p.cut[2 * blockIdx.x], of = p.cut[2 * blockIdx.x + 1];
+    if (cut.x >= 0) {
+        const int b = cut.x, hg = cut.y, u = cut.z, parts = cut.w >> 1;
+        const Kv8Seq seq = {of.x, of.y, of.z};
         const int r = r0 + warp / WPR;
         float m = kNoKey, sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int x0 = warp % WPR; x0 < parts; x0 += 4 * WPR) {
-            float2 ml[4];
-            float4 o[4];
+        for (int x0 = warp % WPR; x0 < parts; x0 += 8 * WPR) {
+            float2 ml[8];
+            float4 o[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const int x = x0 + j * WPR;
                 ml[j] = make_float2(kNoKey, 0.f);
                 o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1104,7 +1094,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine(const Kv8Decod
                 }
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 const float m1 = fmaxf(m, ml[j].x);
                 const float a = ex2_approx(m - m1), f = ex2_approx(ml[j].x - m1);
                 m = m1;
@@ -1118,7 +1108,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine(const Kv8Decod
         reinterpret_cast<float4*>(so[warp])[lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         if (lane == 0) sml[warp] = make_float2(m, sum);
         __syncthreads();
-        for (int x = tid; x < PASS * 128; x += 32 * kCombineWarps) {
+        for (int x = tid; x < CR * 128; x += 32 * kCombineWarps) {
             const int row = x >> 7, dim = x & 127;
             int i, h;
             if (!kv8_row<ROWS, PAIR>(p, seq, hg, u, r0 + row, i, h)) continue;
@@ -1133,7 +1123,19 @@ __global__ void __launch_bounds__(32 * kCombineWarps) kv8_combine(const Kv8Decod
             }
             kv8_store<ROWS, PAIR>(p, seq, b, i, h, r0 + row, dim, out, total, M);
         }
-        __syncthreads();
+    }
+    const int items = p.B * p.groups * p.units;
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int bh = item / p.units, u = item - bh * p.units;
+        const int b = bh / p.groups, hg = bh - b * p.groups;
+        const Kv8Seq seq = kv8_seq(p, b);
+        if (kv8_keys<SUB>(p, seq, u).tiles() > 0) continue;
+        for (int x = tid; x < CR * 128; x += 32 * kCombineWarps) {
+            const int row = r0 + (x >> 7);
+            int i, h;
+            if (kv8_row<ROWS, PAIR>(p, seq, hg, u, row, i, h))
+                kv8_store<ROWS, PAIR>(p, seq, b, i, h, row, x & 127, 0.f, 0.f, kNoKey);
+        }
     }
 }
 

@@ -72,7 +72,7 @@ Kv8Plan kv8_plan(int B, int Sq, int Hq, int Hkv, int D) {
     pl.units = int((sub * heads + pl.rows - 1) / pl.rows);
     pl.items = (long long)B * pl.groups * pl.units;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    pl.off_ml = up(size_t(kKv8MaxCtas) * 16);
+    pl.off_ml = up(size_t(kKv8MaxCtas) * 32);
     pl.off_o = pl.off_ml + up(size_t(kKv8MaxCtas) * 2 * pl.rows * 8);
     pl.bytes = pl.off_o + size_t(kKv8MaxCtas) * 2 * pl.rows * 128 * 4;
     return pl;
@@ -296,8 +296,9 @@ int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const flo
         const int r2 = launch_pdl(gqa::kv8_decode<rows(), pair()>, dim3(grid), C::THREADS,
                                   C::SMEM_BYTES, stream, tk, tv, p);
         if (r2 != GQA_OK) return r2;
-        return launch_pdl(gqa::kv8_combine<rows(), pair()>, dim3(grid), 32 * gqa::kCombineWarps, 0,
-                          stream, p);
+        return launch_pdl(gqa::kv8_combine<rows(), pair()>,
+                          dim3(grid, rows() / gqa::kCombineRows), 32 * gqa::kCombineWarps,
+                          0, stream, p);
     };
     auto pick = [&](auto pair, int bit) {
         using std::integral_constant;
