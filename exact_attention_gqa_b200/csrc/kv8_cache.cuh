@@ -177,22 +177,25 @@ __device__ __forceinline__ float pow2_scale(float a) {
 
 constexpr float kBf16Max = 3.3895313892515355e38f;
 
-// The largest of a and |x| of eight bf16; fmaxf passes over NaN.
-__device__ __forceinline__ float amax8(const uint4& x, float a) {
+// The larger of each half of a and |x| of eight bf16, as two bf16 (the maximum passes over
+// NaN).
+__device__ __forceinline__ uint32_t amax8(const uint4& x, uint32_t a) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        a = fmaxf(a, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+        asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(w[i] & 0x7fff7fffu));
     return a;
 }
 
 // eight bf16 times inv -> eight e4m3 codes (rounded to nearest even, saturating)
 __device__ __forceinline__ uint2 encode8(const uint4& x, float inv) {
-    return make_uint2(
-        pack_e4m3x4(bf16_lo(x.x) * inv, bf16_hi(x.x) * inv, bf16_lo(x.y) * inv,
-                    bf16_hi(x.y) * inv),
-        pack_e4m3x4(bf16_lo(x.z) * inv, bf16_hi(x.z) * inv, bf16_lo(x.w) * inv,
-                    bf16_hi(x.w) * inv));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const uint64_t inv2 = f2_pack(inv, inv);
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f2_unpack(fmul2(f2_pack(bf16_lo(w[i]), bf16_hi(w[i])), inv2), f[2 * i], f[2 * i + 1]);
+    return make_uint2(pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]));
 }
 
 // four codes -> four fp32 (exact)
@@ -310,18 +313,19 @@ __global__ void __launch_bounds__(256, 4) kv8_append(const Kv8AppendParams p) {
         }
     };
     auto finish = [&](const Task& k) {
-        float a = 0.f;
+        uint32_t a2 = 0u;
         bool restart = false;
 #pragma unroll
         for (int j = 0; j < HELD; ++j) {
-            a = amax8(k.held[j], a);
+            a2 = amax8(k.held[j], a2);
             restart |= (k.at[j] & (sb - 1)) == 0;
         }
         for (int i = r + HELD * step; i < k.n; i += step) {
-            a = amax8(load(k, i), a);
+            a2 = amax8(load(k, i), a2);
             restart |= (__ldg(p.slot_map + k.t + i) & (sb - 1)) == 0;
         }
-        a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));  // (a >= 0)
+        // (bits of numbers >= 0 order as the numbers do)
+        float a = __uint_as_float(__reduce_max_sync(0xffffffffu, max(a2 << 16, a2 & 0xffff0000u)));
         restart = __any_sync(0xffffffffu, restart);
         if (team > 1) {
             if (lane == 0) {
@@ -439,20 +443,24 @@ __global__ void __launch_bounds__(256) kv8_gather(const Kv8GatherParams p) {
     const uint32_t chunks = uint32_t(p.Hkv) * p.D / 8;  // of one row
     const uint32_t end = kGatherRows * chunks;
     const int per_head = p.D == 128 ? 4 : 3;  // log2 of a head's chunks
+    const uint32_t rows_on = 256 / chunks, chunks_on = 256 - rows_on * chunks;
+    uint32_t i = threadIdx.x / chunks, c = threadIdx.x - i * chunks;  // this chunk's row, place
     for (uint32_t e0 = threadIdx.x; e0 < end; e0 += 8 * 256) {
         uint2 o[8];
         float f[8];
         uint4* out[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t e = e0 + j * 256, i = e / chunks, c = e - i * chunks;
-            const int s = e < end ? src[i] : -1;
+            const int s = e0 + j * 256 < end ? src[i] : -1;
             out[j] = nullptr;
             if (s >= 0) {
                 o[j] = __ldg(reinterpret_cast<const uint2*>(io.codes + size_t(s) * chunks * 8) + c);
                 f[j] = __ldg(io.scale + size_t(s >> p.sb_shift) * p.Hkv + (c >> per_head));
                 out[j] = reinterpret_cast<uint4*>(io.out + size_t(row0 + i) * chunks * 8) + c;
             }
+            i += rows_on;
+            c += chunks_on;
+            if (c >= chunks) c -= chunks, ++i;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
