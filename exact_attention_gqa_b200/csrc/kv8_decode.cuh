@@ -35,8 +35,16 @@
 // 128 keys, and cut into equal ranges, whatever the lengths.  A range is taken by a team
 // of CTAs, one for each head group (`width` of them): they walk the same keys side by
 // side, so that the 128-byte pieces of one token's row are read at about the same time,
-// which is what DRAM wants.  An item that ends up in several ranges leaves one fp32
-// partial in each, joined by kv8_combine, a programmatic dependent launch.
+// which is what DRAM wants (one query, batch 16 at 32768 keys: 203 us before, 184 with it).
+// An item that ends up in several ranges leaves one fp32 partial in each, joined by
+// kv8_combine, a programmatic dependent launch.
+//
+// Roles: one warp copies and looks pages up, one issues the MMAs, one or two warpgroups do
+// the softmax.
+//
+// Measured (device time in a CUDA graph; 32 query heads on 8, D 128): one query, batch 16 at
+// 32768 keys 161 to 165 us (6.5 to 6.7 TB/s of the cache's data), batch 64 ragged up to 8192
+// 97 us, 8 sequences of up to 8192 with four queries each 35 us, one of 1000 keys 12 us.
 #pragma once
 #include "kv8_cache.cuh"
 
@@ -67,6 +75,9 @@ template <int ROWS>
 struct Kv8Cfg {
     static constexpr int WGS = ROWS >= 16 ? 2 : 1;      // consumer warpgroups, rows split
     static constexpr int RW = ROWS / WGS;               // rows of each
+    // Three CTAs with two stages each, up to 8 rows, measured against two with three: batch
+    // 16 at 32768 keys 182 / 164 us, two queries for 16 at 16384 98.6 / 94.4, ragged batch of
+    // 64 94.6 / 97.4, windows of 2048 (D 64) 34.2 / 35.9.
     static constexpr int CTAS_PER_SM = 2;
     static constexpr int STK = ROWS <= 16 ? 3 : 2;      // stages of K, and of V and scales:
     static constexpr int STV = STK;                     // what fits shared memory
@@ -82,7 +93,7 @@ struct Kv8Cfg {
     static constexpr int OFF_LIM = OFF_ROW + 32 * ROWS;  // [2][ROWS] keys a row sees: from, to
     static constexpr int OFF_TOP = OFF_LIM + 16 * ROWS;  // [2][ROWS] next reference, ordered int
     static constexpr int OFF_VRUN = OFF_TOP + 8 * ROWS;  // [2][2 halves] vrun, log2, 1 / vrun
-    static constexpr int OFF_OUT = OFF_VRUN + 64;        // [2][ROWS] a row's position (-1: none) and head
+    static constexpr int OFF_OUT = OFF_VRUN + 64;        // [2][ROWS] position or -1, head
     static constexpr int OFF_SEG = OFF_OUT + 16 * ROWS;  // [8] Kv8Segment
     static constexpr int OFF_BAR = OFF_SEG + 8 * 64;
     static constexpr int N_BAR = 2 * STK + 3 * STV + 8;
@@ -126,7 +137,9 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8DecodeParams& p, int b) {
 struct Kv8Keys {
     int lo, hi;
     __device__ __forceinline__ int first() const { return lo >> 7; }
-    __device__ __forceinline__ int tiles() const { return hi > lo ? ((hi + 127) >> 7) - (lo >> 7) : 0; }
+    __device__ __forceinline__ int tiles() const {
+        return hi > lo ? ((hi + 127) >> 7) - (lo >> 7) : 0;
+    }
 };
 template <int SUB>
 __device__ __forceinline__ Kv8Keys kv8_keys(const Kv8DecodeParams& p, const Kv8Seq& s, int u) {
@@ -144,8 +157,8 @@ __device__ __forceinline__ Kv8Keys kv8_keys(const Kv8DecodeParams& p, const Kv8S
 // first kItemStart units standing for its start.  Beginning another item (its q, the first
 // tile's two passes, the last one's results) takes a CTA 4 to 6 us, a tile about 1.3; with
 // equal numbers of tiles the CTAs with more items were that much behind.  Measured at 0 / 2 /
-// 3 / 4: window batch of 32 (D 64) 40.8 / 36.3 / 36.1 / 35.4 us, 4 drafted tokens for 8
-// 41.6 / 40.4 / 38.9 / 38.3, ragged batch of 64 98.3 / 97.6 / 96.9 / 97.7.
+// 4: window batch of 32 (D 64) 41.8 / 36.7 / 35.9 us, 4 drafted tokens for 8 38.2 / 36.3 /
+// 34.6, ragged batch of 64 99.4 / 97.5 / 97.4, one sequence of 1000 keys 10.9 / 12.2 / 12.1.
 constexpr int kItemStart = 4;
 __device__ __forceinline__ int kv8_cost(int tiles) { return tiles > 0 ? tiles + kItemStart : 0; }
 // Units are numbered with 31 bits (the host refuses more).  `units` of them go to `teams`
@@ -471,8 +484,13 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         // scales of its eight groups of 16 keys (a scale block is 16 keys or more) of each
         // head.  The warp looks the pages of a batch of tiles up at once, a lane for each
         // tile and box and for each tile, head and group, one batch ahead and across
-        // segments; what it then needs of global memory goes to shared memory by itself
-        // (bulk copies, and asynchronous copies of the scales), so no load holds it up.
+        // segments.
+        // A tile's scales are waited for before its copies go out, on purpose: they lie in a
+        // 32-byte sector that the CTAs of a team share, so that all of them wait for the same
+        // one and stay in step.  With asynchronous copies of the scales nothing held a team
+        // together, its CTAs drifted up to 17 us apart (below 1 here; batch 16, 32768 keys),
+        // the pieces of a token's row were no longer read at the same time, and that batch
+        // took 188 us instead of 164.
         const int team = blockIdx.x / p.width, member = blockIdx.x - team * p.width;
         Kv8Walk<SUB> walk;
         int teams, range;
@@ -801,8 +819,10 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         };
         // Segment -1 is a dry run of one tile on whatever tensor and shared memory hold, with
         // no waits and nothing handed on: it brings the instructions of a tile into the SM's
-        // cache while the first keys are on their way (a kernel starts with none of them,
-        // and fetching them costs up to 3 us).
+        // cache while the first keys are on their way.  Behind other kernels (and a flush of
+        // L2), on an event clock of 2 us steps: one sequence of 1000 keys 20.5 -> 18.4 us, of
+        // 32768 36.9 -> 34.8, larger batches within a step.  In back to back calls, which
+        // find the instructions there, within 1 % (3 % for the one sequence of 32768).
         bool more = true;
         for (int seg = -1; more; ++seg) {
             const Kv8Segment& g = segments[seg & 7];

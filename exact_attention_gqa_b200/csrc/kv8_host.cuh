@@ -166,8 +166,8 @@ int gqa_attn_kv8_append(const void* k, const void* v, const int* slot_map, void*
     p.wide = std::max(1, std::min(8, scale_block / held));
     // CTAs for each 32 tokens: as many as run at a time (four an SM), up to a warp for each
     // (token, K or V, head); for prompts kAppendShare, each with a few tasks then.  2048
-    // single tokens: 18.8 us (22.1 with eight times as many CTAs), prompts of 4 x 8192
-    // tokens: 55.5 us (58.6 with 8 CTAs for each 32).
+    // single tokens: 16.9 us (20.3 with a warp for each task), 4 prompts of up to 8192
+    // tokens: 51.9 us (54.9 with 8 CTAs for each 32, 125 with a warp for each task).
     const int windows = (T + 31) / 32;
     const int all = (32 * 2 * Hkv + 7) / 8;
     const int share =
