@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables(const KvTablesParams
     }
     __syncthreads();
     const int tokens = cu_q[p.B], pages = pg[p.B];
-    auto free_page = [&](long long f) { return f < p.n_free ? __ldg(p.free_pages + f) : -1; };
+    auto free_page = [&](long long f) { return f < p.n_free ? p.free_pages[f] : -1; };
     const int stride = gridDim.x * kTablesThreads;
     for (int f = blockIdx.x * kTablesThreads + tid; f < pages; f += stride) {
         const int b = owner_of(pg, p.B, f);
@@ -239,13 +239,13 @@ __global__ void __launch_bounds__(256, 4) kv8_append(const Kv8AppendParams p) {
     const int sb = 1 << p.sb_shift;
     auto block_of = [&](int t) {  // token t's scale block, -1: none
         if (t < 0 || t >= p.T) return -1;
-        const int s = __ldg(p.slot_map + t);
+        const int s = p.slot_map[t];
         return s >= 0 && s < p.slots ? s >> p.sb_shift : -1;
     };
     const int mine = block_of(t0 + lane), after = block_of(t0 + 32 + lane);
     int before = block_of(t0 - 1);
     if (blockIdx.y == 0 && warp == 0 && mine < 0 && t0 + lane < p.T &&
-        __ldg(p.slot_map + t0 + lane) != -1)
+        p.slot_map[t0 + lane] != -1)
         raise_device_error(kDevBadKvIndex);
     const int left = __shfl_up_sync(0xffffffffu, mine, 1);
     if (lane > 0) before = left;
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(256, 4) kv8_append(const Kv8AppendParams p) {
         int at[HELD];            // the rows' positions in the block
     };
     auto load = [&](const Task& k, int i) {
-        return __ldg(reinterpret_cast<const uint4*>(k.x + (long long)i * k.stride));
+        return *reinterpret_cast<const uint4*>(k.x + (long long)i * k.stride);
     };
     auto fetch = [&](Task& k, int task) {
         const int which = task / p.Hkv, h = task - which * p.Hkv;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(256, 4) kv8_append(const Kv8AppendParams p) {
             k.at[j] = 1;
             if (i < k.n) {
                 k.held[j] = load(k, i);
-                k.at[j] = __ldg(p.slot_map + k.t + i);
+                k.at[j] = p.slot_map[k.t + i];
             }
         }
     };
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(256, 4) kv8_append(const Kv8AppendParams p) {
         }
         for (int i = r + HELD * step; i < k.n; i += step) {
             a2 = amax8(load(k, i), a2);
-            restart |= (__ldg(p.slot_map + k.t + i) & (sb - 1)) == 0;
+            restart |= (p.slot_map[k.t + i] & (sb - 1)) == 0;
         }
         // (bits of numbers >= 0 order as the numbers do)
         float a = __uint_as_float(__reduce_max_sync(0xffffffffu, max(a2 << 16, a2 & 0xffff0000u)));
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(256, 4) kv8_append(const Kv8AppendParams p) {
                 for (int i = r; i < sb; i += step) {
                     bool now = false;  // written by this call
                     for (int j = 0; j < k.n; ++j)
-                        now |= (__ldg(p.slot_map + k.t + j) & (sb - 1)) == i;
+                        now |= (p.slot_map[k.t + j] & (sb - 1)) == i;
                     if (now) continue;
                     uint2* d = reinterpret_cast<uint2*>(k.codes + i * row);
                     const uint2 o = *d;
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(256, 4) kv8_append(const Kv8AppendParams p) {
                 *reinterpret_cast<uint2*>(k.codes + (k.at[j] & (sb - 1)) * row) =
                     encode8(k.held[j], inv);
         for (int i = r + HELD * step; i < k.n; i += step) {
-            const int off = __ldg(p.slot_map + k.t + i) & (sb - 1);
+            const int off = p.slot_map[k.t + i] & (sb - 1);
             *reinterpret_cast<uint2*>(k.codes + off * row) = encode8(load(k, i), inv);
         }
     };
@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(256) kv8_gather(const Kv8GatherParams p) {
         int b = 0, first = 0, end;
         if (p.B <= 32) {  // the lanes hold the prefix sums: one load, five steps of registers
             const int lane = threadIdx.x & 31;
-            const int cu = __ldg(p.cu_seqlens_k + min(lane, p.B - 1));
-            end = __ldg(p.cu_seqlens_k + p.B);
+            const int cu = p.cu_seqlens_k[min(lane, p.B - 1)];
+            end = p.cu_seqlens_k[p.B];
 #pragma unroll
             for (int step = 16; step > 0; step >>= 1) {
                 const int at = __shfl_sync(0xffffffffu, cu, min(b + step, 31));
@@ -428,15 +428,15 @@ __global__ void __launch_bounds__(256) kv8_gather(const Kv8GatherParams p) {
             }
             first = __shfl_sync(0xffffffffu, cu, b);
         } else {
-            end = __ldg(p.cu_seqlens_k + p.B);
+            end = p.cu_seqlens_k[p.B];
             b = owner_of(p.cu_seqlens_k, p.B, t);
-            first = __ldg(p.cu_seqlens_k + b);
+            first = p.cu_seqlens_k[b];
         }
         if (t < p.total && t < end) {
             const int pos = t - first;
             const int lp = pos >> p.page_shift;
             int page = (pos >= 0 && lp < p.max_pages)
-                           ? __ldg(p.block_table + size_t(b) * p.max_pages + lp)
+                           ? p.block_table[size_t(b) * p.max_pages + lp]
                            : -1;
             if (page < 0 || page >= p.num_pages) {
                 raise_device_error(kDevBadKvIndex);
@@ -462,8 +462,8 @@ __global__ void __launch_bounds__(256) kv8_gather(const Kv8GatherParams p) {
             const int s = e0 + j * 256 < end ? src[i] : -1;
             out[j] = nullptr;
             if (s >= 0) {
-                o[j] = __ldg(reinterpret_cast<const uint2*>(io.codes + size_t(s) * chunks * 8) + c);
-                f[j] = __ldg(io.scale + size_t(s >> p.sb_shift) * p.Hkv + (c >> per_head));
+                o[j] = reinterpret_cast<const uint2*>(io.codes + size_t(s) * chunks * 8)[c];
+                f[j] = io.scale[size_t(s >> p.sb_shift) * p.Hkv + (c >> per_head)];
                 out[j] = reinterpret_cast<uint4*>(io.out + size_t(row0 + i) * chunks * 8) + c;
             }
             i += rows_on;

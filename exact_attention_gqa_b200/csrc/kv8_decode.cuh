@@ -117,15 +117,15 @@ __device__ __forceinline__ Kv8Seq kv8_seq(const Kv8DecodeParams& p, int b) {
     s.q0 = b * p.Sq;
     s.n = p.Sq;
     if (p.cu_seqlens_q) {
-        s.q0 = __ldg(p.cu_seqlens_q + b);
-        s.n = __ldg(p.cu_seqlens_q + b + 1) - s.q0;
+        s.q0 = p.cu_seqlens_q[b];
+        s.n = p.cu_seqlens_q[b + 1] - s.q0;
         if (s.n < 0 || s.n > p.Sq || s.q0 < 0 || s.q0 > p.total_q - s.n) {
             raise_device_error(kDevBadTile);
             s.n = 0;
         }
     }
     const int cap = p.max_pages << p.page_shift;
-    s.len = __ldg(p.seqlens_k + b);
+    s.len = p.seqlens_k[b];
     if (s.len < 0 || s.len > cap) {
         raise_device_error(kDevBadKvIndex);
         s.len = min(max(s.len, 0), cap);
@@ -566,8 +566,8 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             const int t = x.t + mine, a = t * 128 + grp * box;
             const int key = a < x.hi && a + box > x.lo ? a : max(x.lo, t * 128);
             // (a lane without a box or a group reads the row's first entry, and uses none)
-            box_page = __ldg(row + (copies(x) ? key >> p.page_shift : 0));
-            grp_page = __ldg(row + (seen(x) ? (t * 128 + grp * 16) >> p.page_shift : 0));
+            box_page = row[copies(x) ? key >> p.page_shift : 0];
+            grp_page = row[seen(x) ? (t * 128 + grp * 16) >> p.page_shift : 0];
         };
         auto slot = [&](int page, int at) {
             if (page < 0 || page >= p.num_pages) {
@@ -607,8 +607,8 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 const bool turn = mine == t - now.t;  // this lane's tile
                 float ks = 0.f, vs = 0.f;
                 if (turn && seen_now) {
-                    ks = __ldg(p.k_scale + scale_at);
-                    vs = __ldg(p.v_scale + scale_at);
+                    ks = p.k_scale[scale_at];
+                    vs = p.v_scale[scale_at];
                 }
                 const int sk = c % C::STK, s = c % C::STV;
                 ok = mbar_wait_warp(s_done + sk, ((c / C::STK) & 1) ^ 1, abort_flag);
@@ -772,8 +772,8 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     const bool valid = kv8_row<ROWS, PAIR>(p, g.seq, g.hg, g.u, r, i, h);
                     w[j] = make_uint2(0u, 0u);
                     if (valid && (!PAIR || (lane >> 4) == r / SUB))
-                        w[j] = __ldg(reinterpret_cast<const uint2*>(
-                            p.q + (size_t(g.seq.q0 + i) * p.Hq + h) * D + d0));
+                        w[j] = *reinterpret_cast<const uint2*>(
+                            p.q + (size_t(g.seq.q0 + i) * p.Hq + h) * D + d0);
                     if (lane == 0) {
                         const int end = g.seq.len - g.seq.n + i + 1;
                         all_limits[buf * ROWS + r] =

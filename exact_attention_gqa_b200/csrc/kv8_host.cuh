@@ -37,7 +37,9 @@ bool make_map_kv8(CUtensorMap* m, const void* base, long long rows, int width, i
 }
 
 // A launch that may begin while the kernel before it in the stream ends: every kernel of
-// this file waits for that one (griddep_wait) before it touches global memory.
+// this file waits for that one (griddep_wait) before it touches global memory, and reads it
+// by ordinary loads: read-only ones (__ldg) are for data that nothing writes while the kernel
+// is there, and this one may be there while the one before it writes.
 template <typename... Params, typename... Args>
 int launch_pdl(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t stream,
                const Args&... args) {

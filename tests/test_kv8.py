@@ -1,6 +1,7 @@
 """Host-side checks of the 8-bit paged cache's entry points: what they refuse, and the
 plain forms the GPU tests compare with.  No compute call is made here."""
 import ctypes
+import pathlib
 
 import numpy as np
 import pytest
@@ -188,6 +189,14 @@ def test_front_end_refuses_other_pools():
                       ((k8, v8, ks, vs[:, :1]), "k_scale")):
         with pytest.raises(ValueError, match=what):
             G.gqa_attn_kv8_append(k, k, i, *bad)
+
+
+def test_kernels_that_start_early_use_no_read_only_loads():
+    """They are resident while the kernel before them may still write what they read, which
+    ld.global.nc does not allow, whatever its place after the wait in the source."""
+    csrc = pathlib.Path(__file__).resolve().parents[1] / "exact_attention_gqa_b200" / "csrc"
+    for name in ("kv8_cache.cuh", "kv8_decode.cuh"):
+        assert "__ldg(" not in (csrc / name).read_text(), name
 
 
 def test_plain_encoder_agrees_with_torch():
