@@ -27,9 +27,11 @@
 // above the maxima are taken over all keys (a warp reduction a row, and an exchange), what
 // is summed so far is rescaled and the tile computed again.
 //
-// Heads of 64 dimensions go in pairs: a 128-byte row holds two KV heads, each query row is
-// padded with zeros in the other's half, and each half of O^T is read by its own head's
-// rows (the MMA's idle half costs nothing here).
+// Heads of 64 dimensions go in pairs: a 128-byte row holds two KV heads.  Of the four MMAs
+// over a row's bytes (K = 32), two are one head's and two the other's, each pair with its own
+// head's query columns: no head meets the other's codes, which a padding with zeros would not
+// keep out (NaN times 0).  Each half of O^T is read by its own head's rows (the MMA's idle
+// half costs nothing here).
 //
 // Work: the (sequence, row unit) items of one head group are laid end to end, in tiles of
 // 128 keys, and cut into equal ranges, whatever the lengths.  A range is taken by a team
@@ -83,10 +85,11 @@ struct Kv8Cfg {
     static constexpr int STV = STK;                     // what fits shared memory
     static constexpr int TILE = 128 * 128;              // bytes of K or V per stage
     static constexpr int N = ROWS <= 8 ? 16 : 2 * ROWS;  // MMA columns: hi and lo of each row
+    static constexpr int NQ = ROWS <= 8 ? 32 : 2 * ROWS;  // q's: of a pair, N / 2 or 16 a head
     static constexpr int OFF_K = 0;
     static constexpr int OFF_V = STK * TILE;
     static constexpr int OFF_Q = OFF_V + STV * TILE;
-    static constexpr int OFF_P = OFF_Q + N * 128;       // two buffers
+    static constexpr int OFF_P = OFF_Q + NQ * 128;      // two buffers
     static constexpr int OFF_SC = OFF_P + 2 * N * 128;  // [STV][K, V][2 halves][8 groups]
     static constexpr int OFF_RED = OFF_SC + STV * 128;  // [ROWS][4 warps]
     static constexpr int OFF_ROW = OFF_RED + 16 * ROWS;  // [2][2][ROWS] logit factor, reference
@@ -99,7 +102,7 @@ struct Kv8Cfg {
     static constexpr int N_BAR = 2 * STK + 3 * STV + 8;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
     static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
-    static constexpr int TMEM_COLS = N == 16 ? 64 : 4 * N;  // two of S^T, one of O^T
+    static constexpr int TMEM_COLS = NQ == 32 ? 128 : 4 * N;  // two of S^T, one of O^T
     static constexpr int CONSUMERS = 128 * WGS;
     static constexpr int THREADS = CONSUMERS + 64;      // and the producer's and the MMA warp
     static_assert((SMEM_BYTES + 1024) * CTAS_PER_SM <= 228 * 1024, "shared memory of an SM");
@@ -329,6 +332,41 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, int r0, float (&hi)
     for (int i = 0; i < C; ++i) {
         hi[i] = __uint_as_float(a[i]);
         lo[i] = __uint_as_float(C == 8 ? b[i] : a[4 + i]);
+    }
+}
+// Logits (hi and lo terms) of rows r0 .. of S^T.  Of a pair's columns, NQ / 2 are each head's:
+// hi of its rows, then lo.
+template <int ROWS, bool PAIR, int C>
+__device__ __forceinline__ void tmem_ld_logits(uint32_t taddr, int r0, float (&hi)[C],
+                                               float (&lo)[C]) {
+    if constexpr (!PAIR) {
+        tmem_ld_rows<ROWS, C>(taddr, r0, hi, lo);
+    } else {
+        constexpr int SUB = ROWS / 2, HALF = Kv8Cfg<ROWS>::NQ / 2;
+        uint32_t a[8], b[8];
+        if constexpr (C > SUB) {  // these are rows of both heads
+            static_assert(C == 2 * SUB && C <= 8, "");
+            tmem_ld8(taddr, a);
+            tmem_ld8(taddr + HALF, b);
+        } else {  // of one
+            static_assert(C == 8 && SUB % 8 == 0, "");
+            const uint32_t at = taddr + r0 / SUB * HALF + r0 % SUB;
+            tmem_ld8(at, a);
+            tmem_ld8(at + SUB, b);
+        }
+        tmem_ld_wait();
+        reg_fence(a);
+        reg_fence(b);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            if constexpr (C > SUB) {
+                hi[i] = __uint_as_float(i < SUB ? a[i] : b[i - SUB]);
+                lo[i] = __uint_as_float(i < SUB ? a[SUB + i] : b[i]);
+            } else {
+                hi[i] = __uint_as_float(a[i]);
+                lo[i] = __uint_as_float(b[i]);
+            }
+        }
     }
 }
 template <int ROWS, int C>
@@ -668,7 +706,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         // the last has left the buffer; P V as soon as P and the values are.  (Issuing four
         // MMAs takes a few hundred cycles, so no consumer does it.)
         if (lane == 0) {
-            const uint32_t idesc_s = idesc_e4m3_f32(128, C::N, 0, 0);
+            const uint32_t idesc_s = idesc_e4m3_f32(128, PAIR ? C::NQ / 2 : C::N, 0, 0);
             const uint32_t idesc_o = idesc_e4m3_f32(128, C::N, 1, 1);
             const uint64_t dk = sw128_desc(smem_u32(smem + C::OFF_K), 16, 1024);
             const uint64_t dv = sw128_desc(smem_u32(smem + C::OFF_V), C::TILE, 1024);
@@ -688,10 +726,13 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     if (x < end && x < y + 2 && mbar_test(full_k + x % C::STK, (x / C::STK) & 1)) {
                         tc_fence_after();
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            umma_ss_f8(tmem + (x & 1) * C::N,
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const int col = PAIR ? (kk >> 1) * (C::NQ / 2) : 0;
+                            umma_ss_f8(tmem + (x & 1) * C::NQ + col,
                                        dk + (((x % C::STK) * C::TILE + kk * 32) >> 4),
-                                       dq + ((kk * 32) >> 4), idesc_s, kk > 0);
+                                       dq + ((col * 128 + kk * 32) >> 4), idesc_s,
+                                       PAIR ? kk & 1 : kk > 0);
+                        }
                         umma_commit(s_done + x % C::STK);
                         ++x;
                     }
@@ -700,7 +741,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                         tc_fence_after();
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            umma_ss_f8(tmem + 2 * C::N,
+                            umma_ss_f8(tmem + 2 * C::NQ,
                                        dv + (((y % C::STV) * C::TILE + kk * 32 * 128) >> 4),
                                        dp + (((y & 1) * (C::N * 128) + kk * 512) >> 4), idesc_o,
                                        y > first || kk > 0);
@@ -730,7 +771,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         // P is [N / 16 chunks][128 keys][16 columns]: a thread stores its key's columns whole
         const uint32_t sp = smem_u32(smem + C::OFF_P) + t128 * 16;
         const uint32_t t_s = tmem + (uint32_t((warp & 3) * 32) << 16);  // this warp's lanes
-        const uint32_t t_o = t_s + 2 * C::N;
+        const uint32_t t_o = t_s + 2 * C::NQ;
         float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
         float2* const all_rows = reinterpret_cast<float2*>(smem + C::OFF_ROW);
         int2* const all_limits = reinterpret_cast<int2*>(smem + C::OFF_LIM);
@@ -801,8 +842,14 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                                      "r"(codes)
                                      : "memory");
                     };
-                    put(r, hi);
-                    put(ROWS + r, lo);
+                    if constexpr (PAIR) {  // (a lane's dimensions are in its head's half)
+                        const int col = r / SUB * (C::NQ / 2) + r % SUB;
+                        put(col, hi);
+                        put(col + SUB, lo);
+                    } else {
+                        put(r, hi);
+                        put(ROWS + r, lo);
+                    }
                     // a row with an infinity or a NaN has no factor: its logits are NaN
                     if (lane == 0)
                         all_rows[(buf * 2 + gen) * ROWS + r] = make_float2(
@@ -864,12 +911,12 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 wait(s_done + c % C::STK, c / C::STK);
                 tc_fence_after();
                 const bool edge = t * 128 < all_lo || t * 128 + 128 > all_hi;
-                const uint32_t t_sc = t_s + (c & 1) * C::N;
+                const uint32_t t_sc = t_s + (c & 1) * C::NQ;
                 const uint32_t sp_c = sp + (c & 1) * (C::N * 128);
                 // logits of rows R0 + r0 .. in log2 units, -inf where not seen
                 auto logits = [&](int r0, float (&f)[CH]) {
                     float lo[CH];
-                    tmem_ld_rows<ROWS, CH>(t_sc, R0 + r0, f, lo);
+                    tmem_ld_logits<ROWS, PAIR, CH>(t_sc, R0 + r0, f, lo);
 #pragma unroll
                     for (int j = 0; j < CH; ++j)
                         f[j] = fmaf(lo[j], 0.0625f, f[j]) *

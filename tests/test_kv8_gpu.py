@@ -372,6 +372,37 @@ def test_decode_wild_scales_of_neighbouring_blocks():
     run_decode(lens, 8, 2, 128, 64, 16, seed=31, cache=cache)
 
 
+def check_decode_nan(got, lse, ref, scale):
+    """NaN exactly where the formula has it, the rest within check_decode's bounds."""
+    assert np.array_equal(np.isnan(got), np.isnan(ref[0]))
+    assert np.array_equal(np.isnan(lse), np.isnan(ref[1]))
+    clean = [np.where(np.isnan(x), 0.0, x) for x in ref]
+    P.check_decode(np.where(np.isnan(got), 0.0, got), np.where(np.isnan(lse), 0.0, lse),
+                   clean, scale)
+
+
+@pytest.mark.parametrize("Hq,H,D", [(2, 2, 64), (4, 4, 64), (8, 4, 64), (12, 3, 64), (16, 2, 64),
+                                    (32, 2, 64), (32, 8, 128)])
+def test_decode_nan_key_of_one_head(Hq, H, D):
+    """It spoils the rows of that head only, at D = 64 not its neighbour's either."""
+    page, block, lens = 16, 16, [300, 129, 5]
+    cache = build_cache(lens, page, block, H, D, 5)
+    kf, table = cache[0].view(-1, H, D), cache[4]
+    for b, pos, h in ((0, 299, H - 1), (1, 0, 0), (2, 4, H // 2)):
+        kf[table[b, pos // page].item() * page + pos % page, h, 3] = 0x7f
+    q = torch.randn(3, 1, Hq, D, generator=torch.Generator().manual_seed(2)).bfloat16()
+    out, lse = G.gqa_attn_kv8_decode(q.to(DEV), *[t.to(DEV) for t in cache], i32(lens))
+    torch.cuda.synchronize()
+    kc, ks, vc, vs = cache_np(*cache[:4], H, D)
+    for b, n in enumerate(lens):
+        row = table[b].tolist()
+        k, v = P.gather(kc, ks, row, n, page, block), P.gather(vc, vs, row, n, page, block)
+        coarse = P.coarse(vc, vs, row, n, page, block)
+        ref = P.decode(q[b].double().numpy(), k, v, 1, 1 / math.sqrt(D), 0, Hq // H, coarse)
+        check_decode_nan(out[b].float().cpu().numpy(), lse[b].T.cpu().numpy(), ref,
+                         1 / math.sqrt(D))
+
+
 def test_decode_empty_batch_and_no_queries():
     cache = [t.to(DEV) for t in build_cache([5], 16, 16, 1, 64, seed=1)]
     q = torch.zeros(0, 1, 2, 64, dtype=torch.bfloat16, device=DEV)
