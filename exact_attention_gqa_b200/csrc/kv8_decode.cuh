@@ -97,7 +97,8 @@ struct Kv8Cfg {
     static constexpr int OFF_TOP = OFF_LIM + 16 * ROWS;  // [2][ROWS] next reference, ordered int
     static constexpr int OFF_VRUN = OFF_TOP + 8 * ROWS;  // [2][2 halves] vrun, log2, 1 / vrun
     static constexpr int OFF_OUT = OFF_VRUN + 64;        // [2][ROWS] position or -1, head
-    static constexpr int OFF_SEG = OFF_OUT + 16 * ROWS;  // [8] Kv8Segment
+    static constexpr int OFF_NAN = OFF_OUT + 16 * ROWS;  // [2][ROWS] dimensions: 128 bits
+    static constexpr int OFF_SEG = OFF_NAN + 32 * ROWS;  // [8] Kv8Segment
     static constexpr int OFF_BAR = OFF_SEG + 8 * 64;
     static constexpr int N_BAR = 2 * STK + 3 * STV + 8;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
@@ -440,6 +441,28 @@ __device__ __forceinline__ bool consumers_any(bool x) {
     return r != 0;
 }
 
+// Bit 7 of each byte that is a NaN code (0x7f or 0xff)
+__device__ __forceinline__ uint32_t nan_codes(uint32_t x) {
+    return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+// Zeroes the NaN codes of V's row for `key` (row n of a tile, 128-byte swizzle) and notes
+// their dimensions, 128 bits a query row, for the rows that see the key.
+template <int ROWS>
+__device__ __noinline__ void take_out_nan(uint32_t* v, int n, int key, const int2* limits,
+                                          uint32_t* noted) {
+    for (int j = 0; j < 32; ++j) {
+        const uint32_t nan = nan_codes(v[j]);
+        if (nan == 0u) continue;
+        v[j] &= ~((nan >> 7) * 0xffu);
+        const int d = (((j >> 2) ^ (n & 7)) << 4) + (j & 3) * 4;
+        const uint32_t bits = (nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) |
+                              (nan >> 28 & 8u);
+        for (int r = 0; r < ROWS; ++r)
+            if (key >= limits[r].x && key < limits[r].y)
+                atomicOr(noted + r * 4 + (d >> 5), bits << (d & 31));
+    }
+}
+
 // Where row `r` of unit u belongs: position i of its sequence and query head h
 template <int ROWS, bool PAIR>
 __device__ __forceinline__ bool kv8_row(const Kv8DecodeParams& p, const Kv8Seq& s, int hg, int u,
@@ -523,7 +546,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         // head.  The warp looks the pages of a batch of tiles up at once, a lane for each
         // tile and box and for each tile, head and group, one batch ahead and across
         // segments.
-        // A tile's scales are waited for before its copies go out, on purpose: they lie in a
+        // A tile's scales are waited for before the next one's copies, on purpose: they lie in a
         // 32-byte sector that the CTAs of a team share, so that all of them wait for the same
         // one and stay in step.  With asynchronous copies of the scales nothing held a team
         // together, its CTAs drifted up to 17 us apart (below 1 here; batch 16, 32768 keys),
@@ -777,6 +800,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         int2* const all_limits = reinterpret_cast<int2*>(smem + C::OFF_LIM);
         int* const all_next = reinterpret_cast<int*>(smem + C::OFF_TOP);
         int2* const all_out = reinterpret_cast<int2*>(smem + C::OFF_OUT);
+        uint32_t* const all_nan = reinterpret_cast<uint32_t*>(smem + C::OFF_NAN);
         float4* const all_vrun = reinterpret_cast<float4*>(smem + C::OFF_VRUN);
         float* so = reinterpret_cast<float*>(smem + C::OFF_P);  // [ROWS][128], P unused
         const int my_half = PAIR ? t128 >> 6 : 0;  // of this thread's dimension
@@ -811,6 +835,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     const int r = warp * MINE + j;
                     int i, h;
                     const bool valid = kv8_row<ROWS, PAIR>(p, g.seq, g.hg, g.u, r, i, h);
+                    if (lane < 4) all_nan[(buf * ROWS + r) * 4 + lane] = 0u;
                     w[j] = make_uint2(0u, 0u);
                     if (valid && (!PAIR || (lane >> 4) == r / SUB))
                         w[j] = *reinterpret_cast<const uint2*>(
@@ -929,16 +954,6 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                         }
                     }
                 };
-                // V rows that no query sees may hold any code: a weight of 0 times NaN
-                // would still reach O
-                if (wg == 0 && !dry && (t * 128 < keys.lo || t * 128 + 128 > keys.hi)) {
-                    wait(full_v + s, c / C::STV);
-                    if (key < keys.lo || key >= keys.hi) {
-                        const uint32_t v = smem_u32(smem + C::OFF_V + s * C::TILE) + t128 * 128;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) st_shared_v4(v + j * 16, 0u, 0u, 0u, 0u);
-                    }
-                }
                 // the weights relative to the rows' references: their terms u, and P
                 float u[RW];
                 for (int pass = 0;; ++pass) {
@@ -1008,6 +1023,29 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                             }
                         }
                         if (lane < RW) atomicMax(next_ref + R0 + lane, ordered(top));
+                    }
+                    // V rows that no query sees may hold any code: a weight of 0 times NaN
+                    // would still reach O.  In a row that only some see, a NaN is taken out
+                    // and noted for those.
+                    if (pass == 0 && wg == 0 && !dry && edge) {
+                        wait(full_v + s, c / C::STV);
+                        uint4* const v = reinterpret_cast<uint4*>(smem + C::OFF_V +
+                                                                  s * C::TILE + t128 * 128);
+                        if (key < keys.lo || key >= keys.hi) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j] = make_uint4(0u, 0u, 0u, 0u);
+                        } else if (key < all_lo || key >= all_hi) {
+                            uint32_t any = 0u;
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint4 x = v[j];
+                                any |= nan_codes(x.x) | nan_codes(x.y) | nan_codes(x.z) |
+                                       nan_codes(x.w);
+                            }
+                            if (any)
+                                take_out_nan<ROWS>(reinterpret_cast<uint32_t*>(v), t128, key,
+                                                   limits, all_nan + (seg & 1) * ROWS * 4);
+                        }
                     }
                     fence_proxy_async();
                     tc_fence_before();
@@ -1095,6 +1133,8 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 const float4 x = reinterpret_cast<float4*>(red)[r];
                 float sum = (x.x + x.y) + (x.z + x.w);
                 float acc = so[r * 128 + t128];
+                if (all_nan[((seg & 1) * ROWS + r) * 4 + (t128 >> 5)] >> (t128 & 31) & 1u)
+                    acc = NAN;
                 // a wait gave up (device error word set): an empty result, so that no stale
                 // memory is picked up
                 if (lost) sum = 0.f, acc = 0.f;

@@ -403,6 +403,44 @@ def test_decode_nan_key_of_one_head(Hq, H, D):
                          1 / math.sqrt(D))
 
 
+@pytest.mark.parametrize("Hq,H,D", [(8, 2, 128), (4, 4, 64), (8, 4, 64), (12, 3, 64), (16, 2, 64),
+                                    (32, 2, 64), (32, 1, 128)])
+@pytest.mark.parametrize("n,window", [(1, 0), (1, 100), (4, 0), (5, 130)])
+def test_decode_nan_codes_reach_only_who_sees_them(Hq, H, D, n, window):
+    """NaN in keys of one head, and in single dimensions of values: at keys that all queries
+    see, only some do, or none (before a window, and not yet for the earlier drafts)."""
+    page, block, lens = 32, 16, [700, 300, 5, 129]
+    cache = build_cache(lens, page, block, H, D, 3)
+    k8, v8, ks, vs, table = cache
+    def at(b, pos):
+        return table[b, pos // page].item() * page + pos % page
+    kf, vf = k8.view(-1, H, D), v8.view(-1, H, D)   # views of the pool
+    nan = 0x7f
+    kf[at(0, 699), H - 1, 5] = nan                # the newest key, one head
+    vf[at(0, 698), 0, 7] = nan                    # a value the first drafts do not see
+    vf[at(0, 699), H - 1, D - 1] = 0xff
+    vf[at(1, 299 - n), 0, 0] = nan                # a value that all see
+    vf[at(1, 180), 0, 33] = nan                   # at a window's edge, or well inside
+    vf[at(1, 299 - 100 + 1), H - 1, 34] = nan
+    vf[at(1, 299 - 130), H - 1, 35] = nan         # seen by the first queries of a window
+    kf[at(2, 4), 0, :] = nan
+    vf[at(2, 3), H - 1, 1:9] = nan
+    g = torch.Generator().manual_seed(11)
+    q = torch.randn(4, n, Hq, D, generator=g).bfloat16()
+    out, lse = G.gqa_attn_kv8_decode(q.to(DEV), *[t.to(DEV) for t in cache], i32(lens),
+                                     window=window)
+    torch.cuda.synchronize()
+    kc, ksn, vc, vsn = cache_np(*cache[:4], H, D)
+    scale = 1 / math.sqrt(D)
+    for b in range(4):
+        row = table[b].tolist()
+        k = P.gather(kc, ksn, row, lens[b], page, block)
+        v = P.gather(vc, vsn, row, lens[b], page, block)
+        coarse = np.nan_to_num(P.coarse(vc, vsn, row, lens[b], page, block))
+        ref = P.decode(q[b].double().numpy(), k, v, n, scale, window, Hq // H, coarse)
+        check_decode_nan(out[b].float().cpu().numpy(), lse[b].T.cpu().numpy(), ref, scale)
+
+
 def test_decode_empty_batch_and_no_queries():
     cache = [t.to(DEV) for t in build_cache([5], 16, 16, 1, 64, seed=1)]
     q = torch.zeros(0, 1, 2, 64, dtype=torch.bfloat16, device=DEV)
