@@ -45,8 +45,8 @@
 // the softmax.
 //
 // Measured (device time in a CUDA graph; 32 query heads on 8, D 128): one query, batch 16 at
-// 32768 keys 161 to 165 us (6.5 to 6.7 TB/s of the cache's data), batch 64 ragged up to 8192
-// 97 us, 8 sequences of up to 8192 with four queries each 35 us, one of 1000 keys 12 us.
+// 32768 keys 165 to 168 us (6.4 to 6.5 TB/s of the cache's data), batch 64 ragged up to 8192
+// 97 us, 8 sequences of up to 8192 with four queries each 36 us, one of 1000 keys 12 us.
 #pragma once
 #include "kv8_cache.cuh"
 
@@ -78,8 +78,8 @@ struct Kv8Cfg {
     static constexpr int WGS = ROWS >= 16 ? 2 : 1;      // consumer warpgroups, rows split
     static constexpr int RW = ROWS / WGS;               // rows of each
     // Three CTAs with two stages each, up to 8 rows, measured against two with three: batch
-    // 16 at 32768 keys 182 / 164 us, two queries for 16 at 16384 98.6 / 94.4, ragged batch of
-    // 64 94.6 / 97.4, windows of 2048 (D 64) 34.2 / 35.9.
+    // 16 at 32768 keys 182 / 165 us, two queries for 16 at 16384 101 / 96.4, ragged batch of
+    // 64 94.8 / 97.3, windows of 2048 (D 64) 36.4 / 37.5.
     static constexpr int CTAS_PER_SM = 2;
     static constexpr int STK = ROWS <= 16 ? 3 : 2;      // stages of K, and of V and scales:
     static constexpr int STV = STK;                     // what fits shared memory
@@ -161,8 +161,8 @@ __device__ __forceinline__ Kv8Keys kv8_keys(const Kv8DecodeParams& p, const Kv8S
 // first kItemStart units standing for its start.  Beginning another item (its q, the first
 // tile's two passes, the last one's results) takes a CTA 4 to 6 us, a tile about 1.3; with
 // equal numbers of tiles the CTAs with more items were that much behind.  Measured at 0 / 2 /
-// 4: window batch of 32 (D 64) 41.8 / 36.7 / 35.9 us, 4 drafted tokens for 8 38.2 / 36.3 /
-// 34.6, ragged batch of 64 99.4 / 97.5 / 97.4, one sequence of 1000 keys 10.9 / 12.2 / 12.1.
+// 4: window batch of 32 (D 64) 43.6 / 38.7 / 37.5 us, 4 drafted tokens for 8 39.8 / 37.9 /
+// 35.6, ragged batch of 64 100.3 / 98.0 / 97.3, one sequence of 1000 keys 11.4 / 12.2 / 12.2.
 constexpr int kItemStart = 4;
 __device__ __forceinline__ int kv8_cost(int tiles) { return tiles > 0 ? tiles + kItemStart : 0; }
 // Units are numbered with 31 bits (the host refuses more).  `units` of them go to `teams`
@@ -666,14 +666,16 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             }
             for (int t = now.t; t < now.t1; ++t, ++c) {
                 const bool turn = mine == t - now.t;  // this lane's tile
+                const int sk = c % C::STK, s = c % C::STV;
+                ok = mbar_wait_warp(s_done + sk, ((c / C::STK) & 1) ^ 1, abort_flag);
+                if (!ok) break;
+                // (here and not before that wait: about 1 %; behind K's or V's copy the ragged
+                // batch of 64 takes 100.9 or 118.3 us instead of 97.3)
                 float ks = 0.f, vs = 0.f;
                 if (turn && seen_now) {
                     ks = p.k_scale[scale_at];
                     vs = p.v_scale[scale_at];
                 }
-                const int sk = c % C::STK, s = c % C::STV;
-                ok = mbar_wait_warp(s_done + sk, ((c / C::STK) & 1) ^ 1, abort_flag);
-                if (!ok) break;
                 if (lane == 0) mbar_arrive_expect_tx(full_k + sk, C::TILE);
                 __syncwarp();
                 if (turn && copies_now)
@@ -892,9 +894,9 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         // Segment -1 is a dry run of one tile on whatever tensor and shared memory hold, with
         // no waits and nothing handed on: it brings the instructions of a tile into the SM's
         // cache while the first keys are on their way.  Behind other kernels (and a flush of
-        // L2), on an event clock of 2 us steps: one sequence of 1000 keys 20.5 -> 18.4 us, of
-        // 32768 36.9 -> 34.8, larger batches within a step.  In back to back calls, which
-        // find the instructions there, within 1 % (3 % for the one sequence of 32768).
+        // L2), on an event clock of 2 us steps: one sequence of 1000 keys 23.6 -> 21.5 us, of
+        // 32768 39.8 -> 35.8, larger batches a step at most.  In back to back calls, which find
+        // the instructions there: windowed batch of 32 39.4 -> 37.5, the other cases 1 to 3 %.
         bool more = true;
         for (int seg = -1; more; ++seg) {
             const Kv8Segment& g = segments[seg & 7];

@@ -521,11 +521,11 @@ int gqa_attn_kv8_gather(const void* k8, const void* v8, const float* k_scale,
  *     pages that hold a visible key are used.
  * All B sequences together: their row units (rows of up to 32 query heads x positions of a
  *     KV head, or of two KV heads at D = 64) times max_pages * page_size / 128 below 2^31.
- * Scales: any finite normal positive fp32.  What lies in the pool outside the visible keys is
- * never used, whatever its codes.  workspace: gqa_attn_kv8_decode_workspace_bytes(B, Sq, Hq,
- * Hkv, D) bytes, 16-byte aligned, private to the call until it has run: a parameter and
- * not the registered workspace, so that calls on several streams and in several captured
- * graphs do not share one.
+ * Scales: any finite normal positive fp32.  What lies in the pool outside the keys that a
+ * query sees does not reach it, whatever its codes.
+ * workspace: gqa_attn_kv8_decode_workspace_bytes(B, Sq, Hq, Hkv, D) bytes, 16-byte aligned,
+ * private to the call until it has run: a parameter and not the registered workspace, so
+ * that calls on several streams and in several captured graphs do not share one.
  */
 size_t gqa_attn_kv8_decode_workspace_bytes(int B, int Sq, int Hq, int Hkv, int D);
 int gqa_attn_kv8_decode(const void* q, const void* k8, const void* v8, const float* k_scale,
