@@ -441,6 +441,30 @@ def test_decode_nan_codes_reach_only_who_sees_them(Hq, H, D, n, window):
         check_decode_nan(out[b].float().cpu().numpy(), lse[b].T.cpu().numpy(), ref, scale)
 
 
+@pytest.mark.parametrize("Hq,H,D", [(4, 2, 128), (8, 2, 64)])
+def test_decode_nan_codes_in_many_short_sequences(Hq, H, D):
+    """The same where a CTA takes several sequences, one after the other, each whole."""
+    page, block, n, B = 16, 16, 3, 640
+    lens = [(37 * b) % 150 + 3 for b in range(B)]
+    cache = build_cache(lens, page, block, H, D, 8)
+    vf, table = cache[1].view(-1, H, D), cache[4]
+    for b in range(0, B, 3):  # the newest value, in a dimension of the sequence's own
+        pos = lens[b] - 1
+        vf[table[b, pos // page].item() * page + pos % page, b % H, b % D] = 0x7f
+    q = torch.randn(B, n, Hq, D, generator=torch.Generator().manual_seed(4)).bfloat16()
+    out, lse = G.gqa_attn_kv8_decode(q.to(DEV), *[t.to(DEV) for t in cache], i32(lens))
+    torch.cuda.synchronize()
+    kc, ks, vc, vs = cache_np(*cache[:4], H, D)
+    out, lse = out.float().cpu().numpy(), lse.cpu().numpy()
+    for b in range(B):
+        row = table[b].tolist()
+        k = P.gather(kc, ks, row, lens[b], page, block)
+        v = P.gather(vc, vs, row, lens[b], page, block)
+        coarse = np.nan_to_num(P.coarse(vc, vs, row, lens[b], page, block))
+        ref = P.decode(q[b].double().numpy(), k, v, n, 1 / math.sqrt(D), 0, Hq // H, coarse)
+        check_decode_nan(out[b], lse[b].T, ref, 1 / math.sqrt(D))
+
+
 def test_decode_empty_batch_and_no_queries():
     cache = [t.to(DEV) for t in build_cache([5], 16, 16, 1, 64, seed=1)]
     q = torch.zeros(0, 1, 2, 64, dtype=torch.bfloat16, device=DEV)
