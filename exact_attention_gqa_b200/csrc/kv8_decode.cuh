@@ -19,13 +19,15 @@
 // Scales: a key's K scale multiplies its logit.  Its V scale is folded into its weight,
 // relative to the largest V scale met so far (vrun), so that O^T can stay in tensor memory
 // and be summed there by the MMA.  With z the logit in log2 units and d = log2(vs / vrun),
-// a row's reference m is kept at or above max_j (z_j + max(d_j, -60)) - 3: weights
+// a row's reference m is kept at or above max_j (z_j + max(d_j, -90)) - 3: weights
 // 32 * 2^(z - m) vs / vrun stay at or below 256 where they are rounded, and the
-// normaliser's terms 2^(z - m) at or below 2^63, however unlike the scales of neighbouring
-// blocks are.  The 3 let references and vrun stay as they are in most tiles: a tile is
-// computed with the last ones, every thread checks its own keys, and only where one is
-// above the maxima are taken over all keys (a warp reduction a row, and an exchange), what
-// is summed so far is rescaled and the tile computed again.
+// normaliser's terms 2^(z - m) at or below 2^93.  The 3 let references and vrun stay as they
+// are in most tiles: a tile is computed with the last ones, every thread checks its own keys,
+// and only where one is above the maxima are taken over all keys (a warp reduction a row, and
+// an exchange), what is summed so far is rescaled and the tile computed again.  Where vrun
+// grows by 2^e all d fall by e, so m falls with them, down to what the tile's own keys and
+// the normaliser ask for: the row of a head that does not attend to the coarse block keeps
+// its weights' size, although another row of its KV head made vrun grow.
 //
 // Heads of 64 dimensions go in pairs: a 128-byte row holds two KV heads.  Of the four MMAs
 // over a row's bytes (K = 32), two are one head's and two the other's, each pair with its own
@@ -112,6 +114,11 @@ struct Kv8Cfg {
 
 // Reference of a row that no key has reached: any logit is above it, and it stays finite
 constexpr float kNoKey = -1e30f;
+// Reference of a row that pads a pass: no logit is above it, and no weight is seen in fp32
+constexpr float kNoRow = 1e30f;
+// How far below vrun a V scale may lie (log2) and its keys' logits still set the reference:
+// the normaliser's terms reach 2^(3 - kFar), and 2^30 keys of them fp32's range
+constexpr float kFar = -90.f;
 
 struct Kv8Seq {
     int q0, n, len;  // first query row, queries, keys
@@ -846,7 +853,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                         const int end = g.seq.len - g.seq.n + i + 1;
                         all_limits[buf * ROWS + r] =
                             make_int2(p.window > 0 ? end - p.window : 0, min(end, g.keys.hi));
-                        all_next[buf * ROWS + r] = ordered(kNoKey);
+                        all_next[buf * ROWS + r] = ordered(-INFINITY);
                         all_out[buf * ROWS + r] = make_int2(valid ? i : -1, h);
                     }
                 }
@@ -883,7 +890,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                             amax >= 0x7f800000u
                                 ? NAN
                                 : __uint_as_float(uint32_t(e - 7) << 23) * p.scale_log2,
-                            kNoKey);
+                            all_out[buf * ROWS + r].x >= 0 ? kNoKey : kNoRow);
                 }
                 fence_proxy_async();
             }
@@ -958,6 +965,35 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 };
                 // the weights relative to the rows' references: their terms u, and P
                 float u[RW];
+                float fall[NH];  // log2 of vrun's growth, where it grows
+                // the next references, from all keys of the tile (next_ref is at -inf)
+                auto raise_refs = [&]() {
+                    float d[NH];  // relative to what vrun becomes
+#pragma unroll
+                    for (int j = 0; j < NH; ++j) {
+                        const float v0 = t > t0 ? vrun[half0 + j].x : 0.f;
+                        const float now = __log2f(fmaxf(vref[j], v0));
+                        d[j] = fmaxf(sc[j].y - now, kFar);
+                        fall[j] = t > t0 && vref[j] > v0 ? fminf(now - vrun[half0 + j].y, 1000.f)
+                                                         : 0.f;
+                    }
+                    float top = -INFINITY;  // lane r: what this warp's keys ask of row r
+#pragma unroll
+                    for (int r0 = 0; r0 < RW; r0 += CH) {
+                        float f[CH];
+                        logits(r0, f);
+#pragma unroll
+                        for (int j = 0; j < CH; ++j) {
+                            const int r = r0 + j;
+                            float mx = warp_max(f[j] + d[half_of(r)]);
+                            // (of the keys before them, what keeps the normaliser's terms small)
+                            if (t > t0)
+                                mx = fmaxf(mx, rows[R0 + r].y + __log2f(warp_max(l[r])) + kFar);
+                            if (lane == r) top = mx;
+                        }
+                    }
+                    if (lane < RW) atomicMax(next_ref + R0 + lane, ordered(top));
+                };
                 for (int pass = 0;; ++pass) {
                     bool high = pass == 0;
                     if (pass > 0 || t > t0) {
@@ -967,7 +1003,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                         for (int j = 0; j < NH; ++j) {
                             const float4 v = vrun[half0 + j];
                             above[j] = -INFINITY;
-                            d[j] = fmaxf(sc[j].y - v.y, -60.f);
+                            d[j] = fmaxf(sc[j].y - v.y, kFar);
                             g[j] = sc[j].z * v.z * 32.f;
                         }
 #pragma unroll
@@ -1001,31 +1037,13 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                             st_shared_v4(sp_c + wg * 2048, hi[0], hi[1], hi[2], hi[3]);
                             st_shared_v4(sp_c + (2 + wg) * 2048, lo[0], lo[1], lo[2], lo[3]);
                         }
-                        // (the second pass has its tile's own references)
-                        high = pass == 0 &&
-                               (above[0] + d[0] > 3.f || above[NH - 1] + d[NH - 1] > 3.f);
+                        // (the second pass has its tile's own references; a scale more than
+                        // 2^60 above vrun is taken up in any case, so that no fp32 weight that
+                        // counts is lost below 2^-126)
+                        high = pass == 0 && (fmaxf(above[0], -57.f) + d[0] > 3.f ||
+                                             fmaxf(above[NH - 1], -57.f) + d[NH - 1] > 3.f);
                     }
-                    if (__any_sync(0xffffffffu, high)) {
-                        float d[NH];  // relative to what vrun becomes
-#pragma unroll
-                        for (int j = 0; j < NH; ++j)
-                            d[j] = fmaxf(
-                                sc[j].y - __log2f(t == t0 ? vref[j]
-                                                          : fmaxf(vref[j], vrun[half0 + j].x)),
-                                -60.f);
-                        float top = -INFINITY;  // lane r: the warp's largest z + d of row r
-#pragma unroll
-                        for (int r0 = 0; r0 < RW; r0 += CH) {
-                            float f[CH];
-                            logits(r0, f);
-#pragma unroll
-                            for (int j = 0; j < CH; ++j) {
-                                const float mx = warp_max(f[j] + d[half_of(r0 + j)]);
-                                if (lane == r0 + j) top = mx;
-                            }
-                        }
-                        if (lane < RW) atomicMax(next_ref + R0 + lane, ordered(top));
-                    }
+                    if (pass == 0 && t == t0) raise_refs();
                     // V rows that no query sees may hold any code: a weight of 0 times NaN
                     // would still reach O.  In a row that only some see, a NaN is taken out
                     // and noted for those.
@@ -1052,7 +1070,11 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     fence_proxy_async();
                     tc_fence_before();
                     if (!consumers_any<CT>(high)) break;
-                    if (t > t0) wait_o(c - 1);
+                    if (t > t0) {
+                        raise_refs();
+                        wait_o(c - 1);
+                        consumers_sync<CT>();
+                    }
                     tc_fence_after();
                     gen ^= 1;
                     float2* const new_rows = all_rows + ((seg & 1) * 2 + gen) * ROWS;
@@ -1064,15 +1086,21 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                         v[j] = fmaxf(vref[j], v0);
                         ratio[j] = v[j] > 0.f ? v0 / v[j] : 0.f;
                     }
+                    auto next_of = [&](int r) {  // of row R0 + r
+                        return fmaxf(fmaxf(rows[R0 + r].y - fall[half_of(r)], kNoKey),
+                                     unordered(next_ref[R0 + r]));
+                    };
 #pragma unroll
                     for (int r0 = 0; r0 < RW; r0 += CH) {
                         float alpha[CH];
 #pragma unroll
                         for (int j = 0; j < CH; ++j) {
                             const int r = r0 + j;
-                            alpha[j] = ex2_approx(rows[R0 + r].y - unordered(next_ref[R0 + r]));
+                            const float next = next_of(r);
+                            alpha[j] = ex2_approx(rows[R0 + r].y - next);
                             l[r] *= alpha[j];
                             alpha[j] *= ratio[half_of(r)];
+                            if (t128 == r) new_rows[R0 + r] = make_float2(rows[R0 + r].x, next);
                         }
                         if (t > t0) {
                             float hi[CH], lo[CH];
@@ -1082,8 +1110,6 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                             tmem_st_rows<ROWS, CH>(t_o, R0 + r0, hi, lo);
                         }
                     }
-                    if (tid < ROWS)
-                        new_rows[tid] = make_float2(rows[tid].x, unordered(next_ref[tid]));
                     if (t128 < NH && (PAIR || wg == 0)) {
                         const float x = t128 ? v[NH - 1] : v[0];
                         new_vrun[half0 + t128] =
@@ -1093,6 +1119,8 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     vrun = new_vrun;
                     tc_fence_before();
                     consumers_sync<CT>();
+                    // (read by all; the next maxima are taken behind another barrier)
+                    if (t128 < RW) next_ref[R0 + t128] = ordered(-INFINITY);
                 }
                 if (tid == 0 && !dry) mbar_arrive(p_ready + (c & 1));
 #pragma unroll
