@@ -17,7 +17,8 @@
 // The terms are further columns of the same MMA, whose N side has room.
 //
 // Scales: a key's K scale multiplies its logit.  Its V scale is folded into its weight,
-// relative to the largest V scale met so far (vrun), so that O^T can stay in tensor memory
+// relative to vrun, the largest V scale met so far or one within 2^3 below it, so that O^T can
+// stay in tensor memory
 // and be summed there by the MMA.  With z the logit in log2 units and d = log2(vs / vrun),
 // a row's reference m is kept at or above max_j (z_j + max(d_j, -90)) - 3: weights
 // 32 * 2^(z - m) vs / vrun stay at or below 256 where they are rounded, and the
@@ -25,9 +26,10 @@
 // are in most tiles: a tile is computed with the last ones, every thread checks its own keys,
 // and only where one is above the maxima are taken over all keys (a warp reduction a row, and
 // an exchange), what is summed so far is rescaled and the tile computed again.  Where vrun
-// grows by 2^e all d fall by e, so m falls with them, down to what the tile's own keys and
-// the normaliser ask for: the row of a head that does not attend to the coarse block keeps
-// its weights' size, although another row of its KV head made vrun grow.
+// grows by 2^e all d fall by e, so m falls with them, down to what the tile's own keys ask for
+// and no further than the normaliser has room: the row of a head that does not attend to the
+// coarse block keeps its weights' size, although another row of its KV head made vrun grow.
+// vrun follows when references are taken anew, and in any case where a scale is 2^3 above it.
 //
 // Heads of 64 dimensions go in pairs: a 128-byte row holds two KV heads.  Of the four MMAs
 // over a row's bytes (K = 32), two are one head's and two the other's, each pair with its own
@@ -97,7 +99,8 @@ struct Kv8Cfg {
     static constexpr int OFF_ROW = OFF_RED + 16 * ROWS;  // [2][2][ROWS] logit factor, reference
     static constexpr int OFF_LIM = OFF_ROW + 32 * ROWS;  // [2][ROWS] keys a row sees: from, to
     static constexpr int OFF_TOP = OFF_LIM + 16 * ROWS;  // [2][ROWS] next reference, ordered int
-    static constexpr int OFF_VRUN = OFF_TOP + 8 * ROWS;  // [2][2 halves] vrun, log2, 1 / vrun
+    static constexpr int OFF_VRUN = OFF_TOP + 8 * ROWS;  // [2][2 halves] vrun, its log2, its
+                                                         // inverse, what counts as far above
     static constexpr int OFF_OUT = OFF_VRUN + 64;        // [2][ROWS] position or -1, head
     static constexpr int OFF_NAN = OFF_OUT + 16 * ROWS;  // [2][ROWS] dimensions: 128 bits
     static constexpr int OFF_SEG = OFF_NAN + 32 * ROWS;  // [8] Kv8Segment
@@ -805,6 +808,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         const uint32_t t_s = tmem + (uint32_t((warp & 3) * 32) << 16);  // this warp's lanes
         const uint32_t t_o = t_s + 2 * C::NQ;
         float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
+        float* l_max = reinterpret_cast<float*>(misc + 4);  // [warps] largest normaliser
         float2* const all_rows = reinterpret_cast<float2*>(smem + C::OFF_ROW);
         int2* const all_limits = reinterpret_cast<int2*>(smem + C::OFF_LIM);
         int* const all_next = reinterpret_cast<int*>(smem + C::OFF_TOP);
@@ -965,38 +969,14 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 };
                 // the weights relative to the rows' references: their terms u, and P
                 float u[RW];
-                float fall[NH];  // log2 of vrun's growth, where it grows
-                // the next references, from all keys of the tile (next_ref is at -inf)
-                auto raise_refs = [&]() {
-                    float d[NH];  // relative to what vrun becomes
+                // Whether this tile has a V scale far above vrun, so that its references are taken
+                // from all of its keys
+                bool far = t == t0;
 #pragma unroll
-                    for (int j = 0; j < NH; ++j) {
-                        const float v0 = t > t0 ? vrun[half0 + j].x : 0.f;
-                        const float now = __log2f(fmaxf(vref[j], v0));
-                        d[j] = fmaxf(sc[j].y - now, kFar);
-                        fall[j] = t > t0 && vref[j] > v0 ? fminf(now - vrun[half0 + j].y, 1000.f)
-                                                         : 0.f;
-                    }
-                    float top = -INFINITY;  // lane r: what this warp's keys ask of row r
-#pragma unroll
-                    for (int r0 = 0; r0 < RW; r0 += CH) {
-                        float f[CH];
-                        logits(r0, f);
-#pragma unroll
-                        for (int j = 0; j < CH; ++j) {
-                            const int r = r0 + j;
-                            float mx = warp_max(f[j] + d[half_of(r)]);
-                            // (of the keys before them, what keeps the normaliser's terms small)
-                            if (t > t0)
-                                mx = fmaxf(mx, rows[R0 + r].y + __log2f(warp_max(l[r])) + kFar);
-                            if (lane == r) top = mx;
-                        }
-                    }
-                    if (lane < RW) atomicMax(next_ref + R0 + lane, ordered(top));
-                };
+                for (int j = 0; j < NH; ++j) far |= vref[j] > vrun[half0 + j].w;
                 for (int pass = 0;; ++pass) {
                     bool high = pass == 0;
-                    if (pass > 0 || t > t0) {
+                    if (pass > 0 || !far) {
                         uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
                         float above[NH], d[NH], g[NH];
 #pragma unroll
@@ -1037,13 +1017,39 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                             st_shared_v4(sp_c + wg * 2048, hi[0], hi[1], hi[2], hi[3]);
                             st_shared_v4(sp_c + (2 + wg) * 2048, lo[0], lo[1], lo[2], lo[3]);
                         }
-                        // (the second pass has its tile's own references; a scale more than
-                        // 2^60 above vrun is taken up in any case, so that no fp32 weight that
-                        // counts is lost below 2^-126)
-                        high = pass == 0 && (fmaxf(above[0], -57.f) + d[0] > 3.f ||
-                                             fmaxf(above[NH - 1], -57.f) + d[NH - 1] > 3.f);
+                        // (the second pass has its tile's own references)
+                        high = pass == 0 &&
+                               (above[0] + d[0] > 3.f || above[NH - 1] + d[NH - 1] > 3.f);
                     }
-                    if (pass == 0 && t == t0) raise_refs();
+                    if (__any_sync(0xffffffffu, high)) {
+                        // what this warp's keys ask of the references (next_ref is at -inf)
+                        float d[NH];  // relative to what vrun becomes
+#pragma unroll
+                        for (int j = 0; j < NH; ++j)
+                            d[j] = fmaxf(
+                                sc[j].y - __log2f(t == t0 ? vref[j]
+                                                          : fmaxf(vref[j], vrun[half0 + j].x)),
+                                kFar);
+                        float top = -INFINITY;  // lane r: the warp's largest z + d of row r
+#pragma unroll
+                        for (int r0 = 0; r0 < RW; r0 += CH) {
+                            float f[CH];
+                            logits(r0, f);
+#pragma unroll
+                            for (int j = 0; j < CH; ++j) {
+                                const float mx = warp_max(f[j] + d[half_of(r0 + j)]);
+                                if (lane == r0 + j) top = mx;
+                            }
+                        }
+                        if (lane < RW) atomicMax(next_ref + R0 + lane, ordered(top));
+                        if (far && t > t0) {
+                            float x = 0.f;
+#pragma unroll
+                            for (int r = 0; r < RW; ++r) x = fmaxf(x, l[r]);
+                            x = warp_max(x);
+                            if (lane == 0) l_max[warp] = x;
+                        }
+                    }
                     // V rows that no query sees may hold any code: a weight of 0 times NaN
                     // would still reach O.  In a row that only some see, a NaN is taken out
                     // and noted for those.
@@ -1070,24 +1076,27 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                     fence_proxy_async();
                     tc_fence_before();
                     if (!consumers_any<CT>(high)) break;
-                    if (t > t0) {
-                        raise_refs();
-                        wait_o(c - 1);
-                        consumers_sync<CT>();
-                    }
+                    if (t > t0) wait_o(c - 1);
                     tc_fence_after();
                     gen ^= 1;
                     float2* const new_rows = all_rows + ((seg & 1) * 2 + gen) * ROWS;
                     float4* const new_vrun = all_vrun + gen * 2;
-                    float v[NH], ratio[NH];
+                    float v[NH], ratio[NH], fall[NH];
 #pragma unroll
                     for (int j = 0; j < NH; ++j) {
                         const float v0 = t > t0 ? vrun[half0 + j].x : 0.f;
                         v[j] = fmaxf(vref[j], v0);
                         ratio[j] = v[j] > 0.f ? v0 / v[j] : 0.f;
+                        fall[j] = t > t0 && vref[j] > v0 ? __log2f(v[j]) - vrun[half0 + j].y : 0.f;
+                        if (far && t > t0) {  // no further than the normaliser has room
+                            const float* x = l_max + wg * 4;
+                            const float most = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+                            fall[j] = fminf(fminf(fall[j], 1000.f),
+                                            fmaxf(-kFar - __log2f(most), 0.f));
+                        }
                     }
-                    auto next_of = [&](int r) {  // of row R0 + r
-                        return fmaxf(fmaxf(rows[R0 + r].y - fall[half_of(r)], kNoKey),
+                    auto next_of = [&](int r, float fall) {  // of row R0 + r
+                        return fmaxf(fmaxf(rows[R0 + r].y - fall, kNoKey),
                                      unordered(next_ref[R0 + r]));
                     };
 #pragma unroll
@@ -1096,11 +1105,9 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
 #pragma unroll
                         for (int j = 0; j < CH; ++j) {
                             const int r = r0 + j;
-                            const float next = next_of(r);
-                            alpha[j] = ex2_approx(rows[R0 + r].y - next);
+                            alpha[j] = ex2_approx(rows[R0 + r].y - next_of(r, fall[half_of(r)]));
                             l[r] *= alpha[j];
                             alpha[j] *= ratio[half_of(r)];
-                            if (t128 == r) new_rows[R0 + r] = make_float2(rows[R0 + r].x, next);
                         }
                         if (t > t0) {
                             float hi[CH], lo[CH];
@@ -1110,10 +1117,15 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                             tmem_st_rows<ROWS, CH>(t_o, R0 + r0, hi, lo);
                         }
                     }
+                    if (t128 < RW)
+                        new_rows[R0 + t128] =
+                            make_float2(rows[R0 + t128].x,
+                                        next_of(t128, half_of(t128) ? fall[NH - 1] : fall[0]));
                     if (t128 < NH && (PAIR || wg == 0)) {
                         const float x = t128 ? v[NH - 1] : v[0];
                         new_vrun[half0 + t128] =
-                            make_float4(x, __log2f(x), x > 0.f ? 1.f / x : 0.f, 0.f);
+                            make_float4(x, __log2f(x), x > 0.f ? 1.f / x : 0.f,
+                                        far ? 8.f * x : vrun[half0 + t128].w);
                     }
                     rows = new_rows;
                     vrun = new_vrun;
