@@ -9,27 +9,31 @@
 // holds what is long,
 //   S^T [128 keys, rows]  = K tile [128 keys, 128 bytes]   x Q^T,
 //   O^T [128 dims, rows]  = V tile^T [128 dims, 128 keys]  x P^T,
-// so that one thread owns one key in the softmax and one dimension in the output.  The bf16
-// (q) and fp32 (p) sides are each split into two e4m3 terms, x = hi + lo / 2^n: e4m3 keeps
-// four significant bits, so hi holds the upper four of bf16's eight, and the remainder, at
-// most half a unit of hi's last place, fits the other term: q is exact (down to 2^-21 of
-// its row's largest element) and p is rounded at 2^-8 of itself, as it would be in bf16.
-// The terms are further columns of the same MMA, whose N side has room.
+// so that one thread owns one key in the softmax and one dimension in the output.  The other
+// sides are split into 8-bit terms, which are further columns of the same MMA (its N side has
+// room).  q, in bf16, is two e4m3 terms, x = hi + lo / 16: e4m3 keeps four significant bits,
+// so hi holds the upper four of bf16's eight and the remainder, at most half a unit of hi's
+// last place, fits the other: q is exact down to 2^-21 of its row's largest element.  p has a
+// range to keep as well, because a long tail of small weights counts: it is rounded to f16,
+// whose upper byte is an e5m2 value of three significant bits, and taken apart into three
+// such, x = hi + mid / 8 + lo / 64.  So p is off by 1.25 * 2^-9 of itself (half a step of
+// nine bits, and f16's own), and by 1.25 * 2^-34 of its row's largest where it is smaller than
+// 2^-25 of that.
 //
 // Scales: a key's K scale multiplies its logit.  Its V scale is folded into its weight,
 // relative to vrun, the largest V scale met so far or one within 2^3 below it, so that O^T can
-// stay in tensor memory
-// and be summed there by the MMA.  With z the logit in log2 units and d = log2(vs / vrun),
-// a row's reference m is kept at or above max_j (z_j + max(d_j, -90)) - 3: weights
-// 32 * 2^(z - m) vs / vrun stay at or below 256 where they are rounded, and the
-// normaliser's terms 2^(z - m) at or below 2^93.  The 3 let references and vrun stay as they
-// are in most tiles: a tile is computed with the last ones, every thread checks its own keys,
-// and only where one is above the maxima are taken over all keys (a warp reduction a row, and
-// an exchange), what is summed so far is rescaled and the tile computed again.  Where vrun
-// grows by 2^e all d fall by e, so m falls with them, down to what the tile's own keys ask for
-// and no further than the normaliser has room: the row of a head that does not attend to the
-// coarse block keeps its weights' size, although another row of its KV head made vrun grow.
-// vrun follows when references are taken anew, and in any case where a scale is 2^3 above it.
+// stay in tensor memory and be summed there by the MMA.  With z the logit in log2 units and
+// d = log2(vs / vrun), a row's reference m is kept at or above max_j (z_j + max(d_j, -90)) - 3:
+// weights 2^11 * 2^(z - m) vs / vrun stay at or below 2^14, where none of their terms leaves
+// e5m2's range, and the normaliser's terms 2^(z - m) at or below 2^96.  The 3 let references
+// and vrun stay as they are in most tiles: a tile is computed with the last ones, every thread
+// checks its own keys, and only where one is above the maxima are taken over all keys (a warp
+// reduction a row, and an exchange), what is summed so far is rescaled and the tile computed
+// again.  Where vrun grows by 2^e all d fall by e, so m falls with them, down to what the
+// tile's own keys ask for and no further than the normaliser has room: the row of a head that
+// does not attend to the coarse block keeps its weights' size, although another row of its KV
+// head made vrun grow.  vrun follows when references are taken anew, and in any case where a
+// scale is 2^3 above it.
 //
 // Heads of 64 dimensions go in pairs: a 128-byte row holds two KV heads.  Of the four MMAs
 // over a row's bytes (K = 32), two are one head's and two the other's, each pair with its own
@@ -85,16 +89,21 @@ struct Kv8Cfg {
     // 16 at 32768 keys 182 / 165 us, two queries for 16 at 16384 101 / 96.4, ragged batch of
     // 64 94.8 / 97.3, windows of 2048 (D 64) 36.4 / 37.5.
     static constexpr int CTAS_PER_SM = 2;
-    static constexpr int STK = ROWS <= 16 ? 3 : 2;      // stages of K, and of V and scales:
-    static constexpr int STV = STK;                     // what fits shared memory
+    // Stages of K, and of V and scales: what fits shared memory.  For 16 rows, 8 x 4 and 16 x 4
+    // drafted: two of K and three of V 37.1 and 116.6 us, three and two 38.0 and 123.0, three
+    // of both with one buffer of P 38.9 and 121.6.
+    static constexpr int STK = ROWS < 16 ? 3 : 2;
+    static constexpr int STV = ROWS <= 16 ? 3 : 2;
     static constexpr int TILE = 128 * 128;              // bytes of K or V per stage
-    static constexpr int N = ROWS <= 8 ? 16 : 2 * ROWS;  // MMA columns: hi and lo of each row
+    static constexpr int N = ROWS <= 8 ? 16 : 2 * ROWS;  // S^T's columns: a row's hi and lo
     static constexpr int NQ = ROWS <= 8 ? 32 : 2 * ROWS;  // q's: of a pair, N / 2 or 16 a head
+    static constexpr int NP = (3 * ROWS + 15) / 16 * 16;  // O^T's and P's: hi, mid and lo
+    static_assert(2 * NP * 128 >= ROWS * 512, "an item's results fit P's buffers");
     static constexpr int OFF_K = 0;
     static constexpr int OFF_V = STK * TILE;
     static constexpr int OFF_Q = OFF_V + STV * TILE;
-    static constexpr int OFF_P = OFF_Q + NQ * 128;      // two buffers
-    static constexpr int OFF_SC = OFF_P + 2 * N * 128;  // [STV][K, V][2 halves][8 groups]
+    static constexpr int OFF_P = OFF_Q + NQ * 128;      // two buffers; an item's results
+    static constexpr int OFF_SC = OFF_P + 2 * NP * 128;  // [STV][K, V][2 halves][8 groups]
     static constexpr int OFF_RED = OFF_SC + STV * 128;  // [ROWS][4 warps]
     static constexpr int OFF_ROW = OFF_RED + 16 * ROWS;  // [2][2][ROWS] logit factor, reference
     static constexpr int OFF_LIM = OFF_ROW + 32 * ROWS;  // [2][ROWS] keys a row sees: from, to
@@ -108,20 +117,26 @@ struct Kv8Cfg {
     static constexpr int N_BAR = 2 * STK + 3 * STV + 8;
     static constexpr int OFF_MISC = OFF_BAR + 8 * N_BAR;
     static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
-    static constexpr int TMEM_COLS = NQ == 32 ? 128 : 4 * N;  // two of S^T, one of O^T
+    static constexpr int TMEM_COLS = NQ == 32 ? 128 : 256;  // two of S^T, one of O^T
     static constexpr int CONSUMERS = 128 * WGS;
     static constexpr int THREADS = CONSUMERS + 64;      // and the producer's and the MMA warp
     static_assert((SMEM_BYTES + 1024) * CTAS_PER_SM <= 228 * 1024, "shared memory of an SM");
-    static_assert(TMEM_COLS * CTAS_PER_SM <= 512, "tensor memory of an SM");
+    static_assert(2 * NQ + NP <= TMEM_COLS && TMEM_COLS * CTAS_PER_SM <= 512, "tensor memory");
 };
+
+// Instruction descriptor, kind::f8f6f4: the B operand's format (bits [10, 13)) e5m2, not e4m3
+constexpr uint32_t kBIsE5m2 = 1u << 10;
 
 // Reference of a row that no key has reached: any logit is above it, and it stays finite
 constexpr float kNoKey = -1e30f;
 // Reference of a row that pads a pass: no logit is above it, and no weight is seen in fp32
 constexpr float kNoRow = 1e30f;
 // How far below vrun a V scale may lie (log2) and its keys' logits still set the reference:
-// the normaliser's terms reach 2^(3 - kFar), and 2^30 keys of them fp32's range
+// the normaliser's terms reach 2^(6 - kFar) (a fall of 3 is not checked), and 2^30 keys of them
+// fp32's range
 constexpr float kFar = -90.f;
+// A weight whose logit is its row's reference and whose V scale is vrun
+constexpr float kTopWeight = 2048.f;
 
 struct Kv8Seq {
     int q0, n, len;  // first query row, queries, keys
@@ -380,19 +395,47 @@ __device__ __forceinline__ void tmem_ld_logits(uint32_t taddr, int r0, float (&h
         }
     }
 }
+// Rows [r0, r0 + C) of O^T, whose column t * ROWS + r is row r's term t (hi, mid, lo): the sums
+// of weights relative to the rows' references, and a rescaling.
 template <int ROWS, int C>
-__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, int r0, const float (&hi)[C],
-                                             const float (&lo)[C]) {
-    uint32_t a[8], b[8];
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        a[i] = __float_as_uint(hi[i]);
-        (C == 8 ? b[i] : a[4 + i]) = __float_as_uint(lo[i]);
+struct OutTerms {
+    static_assert((ROWS == 4 && C == 4) || C == 8, "");
+    static constexpr int LOADS = C == 8 ? 3 : 2;  // of 8 columns: a term, or two of four rows
+    static __device__ __forceinline__ uint32_t column(int r0, int i) {
+        return C == 8 ? i * ROWS + r0 : i * 8;
     }
-    tmem_st8(taddr + r0, a);
-    if constexpr (C == 8) tmem_st8(taddr + ROWS + r0, b);
-    tmem_st_wait();
-}
+    static __device__ __forceinline__ void sum(uint32_t taddr, int r0, float (&x)[C]) {
+        uint32_t a[LOADS][8];
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) tmem_ld8(taddr + column(r0, i), a[i]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) reg_fence(a[i]);
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const float hi = __uint_as_float(a[0][j]);
+            const float mid = __uint_as_float(C == 8 ? a[1][j] : a[0][4 + j]);
+            const float lo = __uint_as_float(a[LOADS - 1][j]);
+            constexpr float k = 1.f / kTopWeight;
+            x[j] = fmaf(lo, k / 64, fmaf(mid, k / 8, hi * k));
+        }
+    }
+    static __device__ __forceinline__ void scale(uint32_t taddr, int r0, const float (&by)[C]) {
+        uint32_t a[LOADS][8];
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) tmem_ld8(taddr + column(r0, i), a[i]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            reg_fence(a[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                a[i][j] = __float_as_uint(__uint_as_float(a[i][j]) * by[j % C]);
+            tmem_st8(taddr + column(r0, i), a[i]);
+        }
+        tmem_st_wait();
+    }
+};
 
 __device__ __forceinline__ void prefetch_l2(const void* at) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
@@ -418,6 +461,28 @@ __device__ __forceinline__ void split_e4m3x4(float x0, float x1, float x2, float
     add_f16x2_to_f32(h01 ^ 0x80008000u, x0, x1);
     add_f16x2_to_f32(h23 ^ 0x80008000u, x2, x3);
     lo = pack_e4m3x4(x0 * shift, x1 * shift, x2 * shift, x3 * shift);
+}
+// Four weights, at most 2^14, as three e5m2 terms each (byte i: weight i), x = hi + mid / 8 +
+// lo / 64.  The upper byte of an f16 is the e5m2 value next to it towards 0; what is left
+// is exact in f16, and eight times that is in range again.  The last term is rounded to
+// nearest: half a unit of a byte is added below it (all terms are >= 0; a NaN stays in hi).
+__device__ __forceinline__ void split_e5m2x4(float x0, float x1, float x2, float x3,
+                                             uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+    uint32_t a, b;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(a) : "f"(x1), "f"(x0));
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(b) : "f"(x3), "f"(x2));
+    hi = __byte_perm(a, b, 0x7531);
+    auto rest = [](uint32_t x) {  // eight times what x's upper bytes leave
+        uint32_t r;
+        asm("{\n\t.reg .b32 t;\n\tsub.f16x2 t, %1, %2;\n\tmul.f16x2 %0, t, %3;\n\t}"
+            : "=r"(r)
+            : "r"(x), "r"(x & 0xff00ff00u), "r"(0x48004800u));
+        return r;
+    };
+    a = rest(a), b = rest(b);
+    mid = __byte_perm(a, b, 0x7531);
+    a = rest(a), b = rest(b);
+    lo = __byte_perm(a + 0x00800080u, b + 0x00800080u, 0x7531);
 }
 // Descriptor of an operand of 16-byte chunks along M or N with no swizzle, the chunks of
 // consecutive k next to each other: kgroup bytes from eight k to the next eight, chunk
@@ -742,11 +807,11 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         // MMAs takes a few hundred cycles, so no consumer does it.)
         if (lane == 0) {
             const uint32_t idesc_s = idesc_e4m3_f32(128, PAIR ? C::NQ / 2 : C::N, 0, 0);
-            const uint32_t idesc_o = idesc_e4m3_f32(128, C::N, 1, 1);
+            const uint32_t idesc_o = idesc_e4m3_f32(128, C::NP, 1, 1) | kBIsE5m2;
             const uint64_t dk = sw128_desc(smem_u32(smem + C::OFF_K), 16, 1024);
             const uint64_t dv = sw128_desc(smem_u32(smem + C::OFF_V), C::TILE, 1024);
             const uint64_t dq = sw128_desc(smem_u32(smem + C::OFF_Q), 16, 1024);
-            // P: [N / 16 chunks][128 keys][16 columns]
+            // P: [NP / 16 chunks][128 keys][16 columns]
             const uint64_t dp = mn_chunk_desc(smem_u32(smem + C::OFF_P), 128, 2048);
             int x = 0, y = 0;  // next tile of S^T, of P V
             bool ok = true;
@@ -778,7 +843,8 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                         for (int kk = 0; kk < 4; ++kk)
                             umma_ss_f8(tmem + 2 * C::NQ,
                                        dv + (((y % C::STV) * C::TILE + kk * 32 * 128) >> 4),
-                                       dp + (((y & 1) * (C::N * 128) + kk * 512) >> 4), idesc_o,
+                                       dp + (((y & 1) * (C::NP * 128) + kk * 512) >> 4),
+                                       idesc_o,
                                        y > first || kk > 0);
                         umma_commit(o_done + y % C::STV);
                         ++y;
@@ -803,7 +869,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         const int wg = warp >> 2;            // this warpgroup's rows: [R0, R0 + RW)
         const int R0 = wg * RW;
         const int t128 = tid & 127;          // this thread's key of a tile, and its dimension
-        // P is [N / 16 chunks][128 keys][16 columns]: a thread stores its key's columns whole
+        // P is [NP / 16 chunks][128 keys][16 columns]: a thread stores its key's columns
         const uint32_t sp = smem_u32(smem + C::OFF_P) + t128 * 16;
         const uint32_t t_s = tmem + (uint32_t((warp & 3) * 32) << 16);  // this warp's lanes
         const uint32_t t_o = t_s + 2 * C::NQ;
@@ -950,7 +1016,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 tc_fence_after();
                 const bool edge = t * 128 < all_lo || t * 128 + 128 > all_hi;
                 const uint32_t t_sc = t_s + (c & 1) * C::NQ;
-                const uint32_t sp_c = sp + (c & 1) * (C::N * 128);
+                const uint32_t sp_c = sp + (c & 1) * (C::NP * 128);
                 // logits of rows R0 + r0 .. in log2 units, -inf where not seen
                 auto logits = [&](int r0, float (&f)[CH]) {
                     float lo[CH];
@@ -977,14 +1043,14 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 for (int pass = 0;; ++pass) {
                     bool high = pass == 0;
                     if (pass > 0 || !far) {
-                        uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};
+                        uint32_t hi[RW / 4], mid[RW / 4], lo[RW / 4];
                         float above[NH], d[NH], g[NH];
 #pragma unroll
                         for (int j = 0; j < NH; ++j) {
                             const float4 v = vrun[half0 + j];
                             above[j] = -INFINITY;
                             d[j] = fmaxf(sc[j].y - v.y, kFar);
-                            g[j] = sc[j].z * v.z * 32.f;
+                            g[j] = sc[j].z * v.z * kTopWeight;
                         }
 #pragma unroll
                         for (int r0 = 0; r0 < RW; r0 += CH) {
@@ -1001,21 +1067,24 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                                     u[r] = ex2_approx(x);
                                     w[e] = u[r] * g[half];
                                 }
-                                split_e4m3x4(w[0], w[1], w[2], w[3], 32.f, hi[(r0 + j) / 4],
-                                             lo[(r0 + j) / 4]);
+                                const int k = (r0 + j) / 4;
+                                split_e5m2x4(w[0], w[1], w[2], w[3], hi[k], mid[k], lo[k]);
                             }
                         }
-                        // columns: hi of every row, then lo
+                        // columns: hi of every row, then mid, then lo
                         if constexpr (RW == 4) {
-                            st_shared_v4(sp_c, hi[0], lo[0], 0u, 0u);
+                            st_shared_v4(sp_c, hi[0], mid[0], lo[0], 0u);
                         } else if constexpr (ROWS == 8) {
-                            st_shared_v4(sp_c, hi[0], hi[1], lo[0], lo[1]);
+                            st_shared_v4(sp_c, hi[0], hi[1], mid[0], mid[1]);
+                            st_shared_v2(sp_c + 2048, lo[0], lo[1]);
                         } else if constexpr (RW == 8) {
                             st_shared_v2(sp_c + R0, hi[0], hi[1]);
-                            st_shared_v2(sp_c + 2048 + R0, lo[0], lo[1]);
+                            st_shared_v2(sp_c + 2048 + R0, mid[0], mid[1]);
+                            st_shared_v2(sp_c + 4096 + R0, lo[0], lo[1]);
                         } else {
                             st_shared_v4(sp_c + wg * 2048, hi[0], hi[1], hi[2], hi[3]);
-                            st_shared_v4(sp_c + (2 + wg) * 2048, lo[0], lo[1], lo[2], lo[3]);
+                            st_shared_v4(sp_c + (2 + wg) * 2048, mid[0], mid[1], mid[2], mid[3]);
+                            st_shared_v4(sp_c + (4 + wg) * 2048, lo[0], lo[1], lo[2], lo[3]);
                         }
                         // (the second pass has its tile's own references)
                         high = pass == 0 &&
@@ -1109,13 +1178,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                             l[r] *= alpha[j];
                             alpha[j] *= ratio[half_of(r)];
                         }
-                        if (t > t0) {
-                            float hi[CH], lo[CH];
-                            tmem_ld_rows<ROWS, CH>(t_o, R0 + r0, hi, lo);
-#pragma unroll
-                            for (int j = 0; j < CH; ++j) hi[j] *= alpha[j], lo[j] *= alpha[j];
-                            tmem_st_rows<ROWS, CH>(t_o, R0 + r0, hi, lo);
-                        }
+                        if (t > t0) OutTerms<ROWS, CH>::scale(t_o, R0 + r0, alpha);
                     }
                     if (t128 < RW)
                         new_rows[R0 + t128] =
@@ -1152,14 +1215,14 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
             tc_fence_after();
             const bool lost = consumers_any<CT>(dead);
             const float2* const rows = all_rows + ((seg & 1) * 2 + gen) * ROWS;
-            const float unit = all_vrun[gen * 2 + my_half].x * 0.03125f;
+            const float unit = all_vrun[gen * 2 + my_half].x;
 #pragma unroll
             for (int r0 = 0; r0 < RW; r0 += CH) {
-                float hi[CH], lo[CH];
-                tmem_ld_rows<ROWS, CH>(t_o, R0 + r0, hi, lo);
+                float o[CH];
+                OutTerms<ROWS, CH>::sum(t_o, R0 + r0, o);
 #pragma unroll
                 for (int j = 0; j < CH; ++j) {  // (so is read back by this thread)
-                    so[(R0 + r0 + j) * 128 + t128] = fmaf(lo[j], 0.03125f, hi[j]) * unit;
+                    so[(R0 + r0 + j) * 128 + t128] = o[j] * unit;
                     float x = l[r0 + j];
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1)

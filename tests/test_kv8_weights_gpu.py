@@ -85,10 +85,12 @@ class Sequence:
         return [torch.stack(x) for x in zip(*out)]
 
 
-# What the kernel's arithmetic allows.  A weight is two e4m3 terms, half a step of the second
-# being 2^-8 of it.
-WEIGHT = 2.0 ** -8
-FLOOR = 0.0
+# What the kernel's arithmetic allows.  A weight is rounded to f16 (half a step, 2^-11 of its
+# power of two) and to nine bits (2^-9).  Where f16 has no normal numbers the steps are 2^-24
+# and 2^-22, half of them 1.25 * 2^-23, and a row's largest weight, its V scale included, is
+# 2^11 or more.
+WEIGHT = 1.25 * 2.0 ** -9
+FLOOR = 1.25 * 2.0 ** -34
 
 
 def check(seq, out, lse, i, ref):
@@ -189,3 +191,77 @@ def test_scales_that_grow_from_tile_to_tile(D, up, down, order, B):
     # within 2^90 from the first tile to the last
     L = 128 * min(6, 1 + 90 // up) - 7
     attend(steps(L, D, up, down, order, seed=up), B)
+
+
+# ------------------------------------------------------------------- peaked rows, long tails
+def sink(L, Hkv, G_, D, drop, spread, seed, sink_value=0.0):
+    """The first key outweighs each other one by `drop` nats and has a value near 0, so that the
+    output is what the tail adds up to: `spread` is its logits' deviation."""
+    z = normal((Hkv, G_, L), seed, spread).clamp(-3 * spread, 3 * spread) - drop
+    z[:, :, 0] = 0
+    v = values(L, Hkv, D, seed + 1)
+    v[0] = sink_value
+    return Sequence(z, v, torch.zeros(-(-L // BLOCK), Hkv, device=DEV), seed + 2)
+
+
+@pytest.mark.parametrize("Hkv,G_,D", [(1, 2, 128), (1, 6, 128), (1, 16, 128), (1, 24, 128),
+                                      (2, 2, 64), (2, 5, 64), (2, 9, 64)])
+@pytest.mark.parametrize("drop", [8, 12, 14, 17])
+@pytest.mark.parametrize("B", [1, 300])
+def test_attention_sink_and_a_long_tail(Hkv, G_, D, drop, B):
+    for L in (1000, 33000):
+        attend(sink(L, Hkv, G_, D, drop, 1.5, seed=L + drop), B)
+
+
+@pytest.mark.parametrize("drop", [14.2, 20])
+@pytest.mark.parametrize("B", [1, 300])
+def test_flat_tails_of_many_keys(drop, B):
+    """All values 1, or 0 at the sink; at 14.2 nats 2^20 keys outweigh it."""
+    for L, value in ((131072, 0.0), (1 << 20, 1.0), (1 << 20, 0.0)):
+        s = sink(L, 1, 2, 64, drop, 0.0, seed=L, sink_value=value)
+        attend(s, B)
+
+
+@pytest.mark.parametrize("window", [0, 2048])
+def test_attention_sink_before_drafted_tokens(window):
+    """And one that leaves the windows of the last queries."""
+    for B in (1, 100):
+        attend(sink(2050, 2, 4, 128, 13, 1.0, seed=B), B, n=4, window=window)
+
+
+@pytest.mark.parametrize("Hkv,G_,D", [(2, 2, 128), (1, 8, 128), (1, 20, 128), (2, 2, 64),
+                                      (4, 7, 64)])
+@pytest.mark.parametrize("spread", [1.0, 4.0])
+@pytest.mark.parametrize("B", [1, 200])
+def test_scales_with_no_order(Hkv, G_, D, spread, B):
+    """Every block's scale between 2^-20 and 2^20, logits near to each other or far apart."""
+    for seed in range(3):
+        L = 5000 + seed
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        z = normal((Hkv, G_, L), seed, spread).clamp(-25, 25)
+        v_exp = torch.randint(-20, 21, (-(-L // BLOCK), Hkv), generator=g, device=DEV)
+        v = values_of(torch.randint(0, 0x7f, (L, Hkv, D), generator=g, device=DEV)
+                      .to(torch.uint8)).float()
+        sign = torch.randint(0, 2, v.shape, generator=g, device=DEV) * 2 - 1
+        attend(Sequence(z, v * sign, v_exp, seed + 9), B)
+
+
+def test_blocks_of_zeros_beside_the_largest_scale():
+    """What appending leaves: blocks of zeros have the scale 2^-126, a block with a value near
+    bf16's largest one of 2^119.  One head attends to it, the other 2^-200 times less."""
+    for at in (0, 10, 30):
+        for B in (1, 200):
+            L = 700
+            z = normal((1, 2, L), at, 0.3)
+            own = slice(at * BLOCK, at * BLOCK + BLOCK)
+            z[0, 0] -= 30
+            z[0, 0, own] = 0
+            z[0, 1] += 40
+            z[0, 1, own] = -100
+            v_exp = torch.full((-(-L // BLOCK), 1), 10.0, device=DEV)
+            v = values(L, 1, 128, at)
+            v_exp[::3] = -126
+            v[(torch.arange(L, device=DEV) // BLOCK) % 3 == 0] = 0
+            v_exp[at] = 119
+            v[own] = 1.5
+            attend(Sequence(z, v, v_exp, at), B)
