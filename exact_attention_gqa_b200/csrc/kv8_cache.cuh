@@ -126,21 +126,23 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables(const KvTablesParams
     __syncthreads();
     const int tokens = cu_q[p.B], pages = pg[p.B];
     auto free_page = [&](long long f) { return f < p.n_free ? p.free_pages[f] : -1; };
-    const int stride = gridDim.x * kTablesThreads;
-    for (int f = blockIdx.x * kTablesThreads + tid; f < pages; f += stride) {
+    // (unsigned: one stride past the largest count is more than an int holds)
+    const unsigned stride = gridDim.x * kTablesThreads;
+    for (unsigned f = blockIdx.x * kTablesThreads + tid; f < unsigned(pages); f += stride) {
         const int b = owner_of(pg, p.B, f);
         int had, add;
         lengths(b, had, add);
-        p.block_table[size_t(b) * p.max_pages + (had + ps - 1) / ps + (f - pg[b])] =
+        p.block_table[size_t(b) * p.max_pages + (had + ps - 1) / ps + (int(f) - pg[b])] =
             free_page((long long)start + f);
     }
-    for (int t = blockIdx.x * kTablesThreads + tid; t < p.max_tokens; t += stride) {
+    for (unsigned t = blockIdx.x * kTablesThreads + tid; t < unsigned(p.max_tokens);
+         t += stride) {
         int slot = -1;
-        if (t < tokens) {
+        if (t < unsigned(tokens)) {
             const int b = owner_of(cu_q, p.B, t);
             int had, add;
             lengths(b, had, add);
-            const int pos = had + (t - cu_q[b]);
+            const int pos = had + (int(t) - cu_q[b]);
             const int lp = pos >> p.page_shift, lp0 = (had + ps - 1) / ps;
             // a page of the cached tokens is in the table already; a new one is not read
             // back from there, because another CTA may be about to write it

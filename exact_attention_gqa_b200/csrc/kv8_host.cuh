@@ -133,8 +133,8 @@ int gqa_attn_kv_tables(const int* cached_lens, const int* new_lens, const int* f
     rc = ensure_smem_limit(gqa::kv_tables, 1 << 19,
                            2 * (kTablesMaxRequests + 1) * int(sizeof(int)));
     if (rc != GQA_OK) return rc;
-    const int want = (max_tokens + gqa::kTablesThreads - 1) / gqa::kTablesThreads;
-    const int grid = std::max(1, std::min(want, dev->sms));
+    const long long want = ((long long)max_tokens + gqa::kTablesThreads - 1) / gqa::kTablesThreads;
+    const int grid = int(std::max(1ll, std::min<long long>(want, dev->sms)));
     return launch_pdl(gqa::kv_tables, dim3(grid), gqa::kTablesThreads, smem, stream, p);
 }
 
