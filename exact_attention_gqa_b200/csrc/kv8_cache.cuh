@@ -146,9 +146,15 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables(const KvTablesParams
             const int lp = pos >> p.page_shift, lp0 = (had + ps - 1) / ps;
             // a page of the cached tokens is in the table already; a new one is not read
             // back from there, because another CTA may be about to write it
-            const int page = lp < lp0 ? p.block_table[size_t(b) * p.max_pages + lp]
-                                      : free_page((long long)start + pg[b] + (lp - lp0));
-            if (page >= 0) slot = int(((long long)page << p.page_shift) + (pos & (ps - 1)));
+            const long long f = (long long)start + pg[b] + (lp - lp0);
+            const bool cached = lp < lp0;
+            const int page =
+                cached ? p.block_table[size_t(b) * p.max_pages + lp] : free_page(f);
+            const long long at = ((long long)page << p.page_shift) + (pos & (ps - 1));
+            if (page >= 0 && at <= INT32_MAX)
+                slot = int(at);
+            else if (cached || f < p.n_free)  // not merely short of pages: no pool has this one
+                raise_device_error(kDevBadKvIndex);
         }
         p.slot_map[t] = slot;
     }

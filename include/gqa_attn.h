@@ -463,7 +463,9 @@ int gqa_attn_decode_fp8(const void* q, const void* k8, const void* v8, float k_s
  * free_end to free_start, and seqlens_k to cached_lens, for the next step.
  * Device error 4: a negative length, one past max_pages * page_size (both are clamped),
  * more tokens than max_tokens (the rest get no slot) or fewer free pages than needed
- * (*free_end > n_free; the entries and slots without a page are -1).  B <= 16384.
+ * (*free_end > n_free; the entries and slots without a page are -1).
+ * Device error 3: a page that no pool holds, negative or with slots past 2^31 - 1, among the
+ * free pages handed out or for a partly filled page; its tokens get no slot.  B <= 16384.
  */
 int gqa_attn_kv_tables(const int* cached_lens, const int* new_lens, const int* free_pages,
                        const int* free_start, int* block_table, int* slot_map, int* seqlens_k,

@@ -38,3 +38,26 @@ def test_the_longest_slot_maps(short_of_2_31):
     assert t.slot_map[43:].max().item() == -1 and t.slot_map[43:].min().item() == -1
     assert table.tolist() == [[5, 3, 9, -1], [1, -1, -1, -1]]
     assert t.cu_seqlens_q.tolist() == [0, 40, 43] and t.free_end.tolist() == [4]
+
+
+@pytest.mark.parametrize("page", [2 ** 26, 2 ** 26 - 1, 2 ** 25, 2 ** 31 - 1, -1, -2 ** 31])
+@pytest.mark.parametrize("cached", [0, 10])
+def test_pages_that_no_pool_holds_get_no_slots(page, cached):
+    """Of 64 tokens each: a slot past 31 bits is not wrapped into another page's."""
+    table = i32([[page if cached else -1, -1], [-1, -1]])
+    free = [2] if cached else [page, 2]
+    t = G.gqa_attn_kv_tables(i32([cached, 0]), i32([3, 2]), i32(free), table, page_size=64,
+                             max_tokens=5)
+    torch.cuda.synchronize()
+    assert gqa_attn_get_device_error() == 3
+    assert t.slot_map.tolist() == [-1, -1, -1, 128, 129]
+    assert table.tolist() == [[page, -1], [2, -1]]
+
+
+def test_slots_up_to_the_last_of_31_bits():
+    table = i32([[2 ** 25 - 1, -1]])
+    t = G.gqa_attn_kv_tables(i32([62]), i32([3]), i32([2 ** 25 - 2]), table, page_size=64,
+                             max_tokens=3)
+    torch.cuda.synchronize()
+    assert gqa_attn_get_device_error() == 0
+    assert t.slot_map.tolist() == [2 ** 31 - 2, 2 ** 31 - 1, 2 ** 31 - 128]
