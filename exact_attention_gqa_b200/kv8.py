@@ -52,6 +52,13 @@ def _refuse(dev, dtype, name, t):
     raise ValueError(f"{name} must be contiguous")
 
 
+def _check_int(**numbers):
+    """Of 31 bits: ctypes would cut a larger one down to 32 bits without a word."""
+    for name, x in numbers.items():
+        if not 0 <= x < 2 ** 31:
+            raise ValueError(f"{name} must be in [0, 2^31)")
+
+
 def _call(torch, name, dev, *args):
     """The C entry point on the current stream of GPU dev, which is made current."""
     fn = getattr(_capi.load(), name)
@@ -101,6 +108,7 @@ def gqa_attn_kv_tables(cached_lens, new_lens, free_pages, block_table, *, page_s
     step's free_start."""
     import torch
 
+    _check_int(max_tokens=max_tokens, page_size=page_size)
     dev, i32 = block_table.get_device(), torch.int32
     if dev < 0:
         _refuse(dev, i32, "block_table", block_table)
@@ -114,8 +122,6 @@ def gqa_attn_kv_tables(cached_lens, new_lens, free_pages, block_table, *, page_s
         _check(dev, i32, free_start=free_start)
         if free_start.numel() != 1:
             raise ValueError("free_start must hold one number")
-    if not 0 <= max_tokens < 2 ** 31:
-        raise ValueError("max_tokens must be in [0, 2^31)")
     # one allocation, cut into the five tables
     sizes = (max_tokens, B, B + 1, B + 1, 1)
     buf = block_table.new_empty(sum(sizes))
@@ -167,14 +173,13 @@ def gqa_attn_kv8_gather(k8, v8, k_scale, v_scale, block_table, cu_seqlens_k, *, 
     GPU; total: its last entry, or more (rows past it stay as they are)."""
     import torch
 
+    _check_int(total=total)
     dev, pages, page, block, Hkv, D = _pool(torch, k8, v8, k_scale, v_scale)
     if cu_seqlens_k.dim() != 1 or cu_seqlens_k.shape[0] < 1:
         raise ValueError("cu_seqlens_k must be [B + 1]")
     B = cu_seqlens_k.shape[0] - 1
     max_pages = _is_table(block_table, B)
     _check(dev, torch.int32, block_table=block_table, cu_seqlens_k=cu_seqlens_k)
-    if not 0 <= total < 2 ** 31:
-        raise ValueError("total must be in [0, 2^31)")
     bf16, shape, out = torch.bfloat16, (total, Hkv, D), []
     for name, t in (("k", k), ("v", v)):
         if t is None:
@@ -207,6 +212,8 @@ def gqa_attn_kv8_decode(q, k8, v8, k_scale, v_scale, block_table, seqlens_k, *,
     Returns (out like q, lse fp32 [B, Hq, Sq], or packed [Hq, total_q])."""
     import torch
 
+    if max_seqlen_q is not None:
+        _check_int(max_seqlen_q=max_seqlen_q)
     dev, pages, page, block, Hkv, D = _pool(torch, k8, v8, k_scale, v_scale)
     i32 = torch.int32
     _check(dev, torch.bfloat16, q=q)
@@ -253,5 +260,5 @@ def gqa_attn_kv8_decode(q, k8, v8, k_scale, v_scale, block_table, seqlens_k, *,
           None if cu_seqlens_q is None else cu_seqlens_q.data_ptr(), out.data_ptr(),
           lse.data_ptr(), ws.data_ptr(), need, B, Sq, total_q, Hq, Hkv, D, pages, page,
           max_pages, block, 1.0 / math.sqrt(D) if scale is None else float(scale),
-          min(int(window), 2 ** 31 - 1))
+          max(min(int(window), 2 ** 31 - 1), -1))
     return out, lse
