@@ -281,10 +281,6 @@ __global__ void __launch_bounds__(256, 4) kv8_append(const Kv8AppendParams p) {
     const int longest = __reduce_max_sync(0xffffffffu, my_n);
     const int team = longest > HELD * RPW ? p.wide : 1;  // warps of a task
     const int teams = 8 / team, my_team = warp / team, wi = warp - my_team * team;
-    auto sync = [&]() {
-        if (team > 1)
-            asm volatile("bar.sync %0, %1;" ::"r"(my_team + 1), "r"(team * 32) : "memory");
-    };
     const int tasks = __popc(leaders) * 2 * p.Hkv;
     const int r = wi * RPW + lane / LPR, c = lane % LPR, step = team * RPW;
     const size_t row = size_t(p.Hkv) * D;

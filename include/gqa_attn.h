@@ -528,9 +528,9 @@ int gqa_attn_kv8_gather(const void* k8, const void* v8, const float* k_scale,
  * Precision: a weight p_j enters the sum over values as f16 would hold p_j * v_scale_j relative
  * to the largest of its row, rounded to nine bits: off by at most 1.25 * 2^-9 of itself, or by
  * 1.25 * 2^-34 of that largest where it is below 2^-25 of it (the sum of the weights, which
- * divides, is not rounded so).  That holds while the V scales of a sequence and head lie within
- * 2^90 of each other, blocks of zeros apart; beside a scale further above the others, what
- * a head has in those loses precision from there on.
+ * divides, is not rounded so).  That holds while the V scales of a sequence and KV head lie
+ * within 2^64 of each other, blocks of zeros apart; beside one further above the others, the
+ * weights of those lose precision from there on.
  * workspace: gqa_attn_kv8_decode_workspace_bytes(B, Sq, Hq, Hkv, D) bytes, 16-byte aligned,
  * private to the call until it has run: a parameter and not the registered workspace, so
  * that calls on several streams and in several captured graphs do not share one.
