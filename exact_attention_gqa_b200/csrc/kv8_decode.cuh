@@ -53,8 +53,8 @@
 // the softmax.
 //
 // Measured (device time in a CUDA graph; 32 query heads on 8, D 128): one query, batch 16 at
-// 32768 keys 165 to 168 us (6.4 to 6.5 TB/s of the cache's data), batch 64 ragged up to 8192
-// 97 us, 8 sequences of up to 8192 with four queries each 36 us, one of 1000 keys 12 us.
+// 32768 keys 168 to 170 us (6.3 to 6.4 TB/s of the cache's data), batch 64 ragged up to 8192
+// 98 us, 8 sequences of up to 8192 with four queries each 38 us, one of 1000 keys 12 us.
 #pragma once
 #include "kv8_cache.cuh"
 
@@ -85,9 +85,9 @@ template <int ROWS>
 struct Kv8Cfg {
     static constexpr int WGS = ROWS >= 16 ? 2 : 1;      // consumer warpgroups, rows split
     static constexpr int RW = ROWS / WGS;               // rows of each
-    // Three CTAs with two stages each, up to 8 rows, measured against two with three: batch
-    // 16 at 32768 keys 182 / 165 us, two queries for 16 at 16384 101 / 96.4, ragged batch of
-    // 64 94.8 / 97.3, windows of 2048 (D 64) 36.4 / 37.5.
+    // Three CTAs with two stages each, for 4 rows (more do not fit), measured against two with
+    // three: batch 16 at 32768 keys 182 / 169 us, ragged batch of 64 95.3 / 97.7, one sequence
+    // of 32768 25.8 / 25.3.
     static constexpr int CTAS_PER_SM = 2;
     // Stages of K, and of V and scales: what fits shared memory.  For 16 rows, 8 x 4 and 16 x 4
     // drafted: two of K and three of V 37.1 and 116.6 us, three and two 38.0 and 123.0, three
@@ -186,8 +186,8 @@ __device__ __forceinline__ Kv8Keys kv8_keys(const Kv8DecodeParams& p, const Kv8S
 // first kItemStart units standing for its start.  Beginning another item (its q, the first
 // tile's two passes, the last one's results) takes a CTA 4 to 6 us, a tile about 1.3; with
 // equal numbers of tiles the CTAs with more items were that much behind.  Measured at 0 / 2 /
-// 4: window batch of 32 (D 64) 43.6 / 38.7 / 37.5 us, 4 drafted tokens for 8 39.8 / 37.9 /
-// 35.6, ragged batch of 64 100.3 / 98.0 / 97.3, one sequence of 1000 keys 11.4 / 12.2 / 12.2.
+// 4: window batch of 32 (D 64) 46.2 / 40.8 / 40.1 us, 4 drafted tokens for 8 41.8 / 39.2 /
+// 37.8, ragged batch of 64 100.7 / 97.6 / 97.7, one sequence of 1000 keys 11.6 / 12.3 / 12.3.
 constexpr int kItemStart = 4;
 __device__ __forceinline__ int kv8_cost(int tiles) { return tiles > 0 ? tiles + kItemStart : 0; }
 // Units are numbered with 31 bits (the host refuses more).  `units` of them go to `teams`
@@ -626,7 +626,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         // one and stay in step.  With asynchronous copies of the scales nothing held a team
         // together, its CTAs drifted up to 17 us apart (below 1 here; batch 16, 32768 keys),
         // the pieces of a token's row were no longer read at the same time, and that batch
-        // took 188 us instead of 164.
+        // took 188 us against 164 at that time.
         const int team = blockIdx.x / p.width, member = blockIdx.x - team * p.width;
         Kv8Walk<SUB> walk;
         int teams, range;
@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                 ok = mbar_wait_warp(s_done + sk, ((c / C::STK) & 1) ^ 1, abort_flag);
                 if (!ok) break;
                 // (here and not before that wait: about 1 %; behind K's or V's copy the ragged
-                // batch of 64 takes 100.9 or 118.3 us instead of 97.3)
+                // batch of 64 takes 101.5 or 119.2 us instead of 97.7, 16 at 32768 keys 166.9 or
+                // 164.4 instead of 168.6)
                 float ks = 0.f, vs = 0.f;
                 if (turn && seen_now) {
                     ks = p.k_scale[scale_at];
@@ -972,8 +973,8 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         // no waits and nothing handed on: it brings the instructions of a tile into the SM's
         // cache while the first keys are on their way.  Behind other kernels (and a flush of
         // L2), on an event clock of 2 us steps: one sequence of 1000 keys 23.6 -> 21.5 us, of
-        // 32768 39.8 -> 35.8, larger batches a step at most.  In back to back calls, which find
-        // the instructions there: windowed batch of 32 39.4 -> 37.5, the other cases 1 to 3 %.
+        // 32768 39.9 -> 37.9, larger batches a step.  In back to back calls, which find the
+        // instructions there: windowed batch of 32 42.1 -> 40.1, the other cases 1 to 4 %.
         bool more = true;
         for (int seg = -1; more; ++seg) {
             const Kv8Segment& g = segments[seg & 7];
