@@ -875,7 +875,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
         const uint32_t t_s = tmem + (uint32_t((warp & 3) * 32) << 16);  // this warp's lanes
         const uint32_t t_o = t_s + 2 * C::NQ;
         float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
-        float* l_max = reinterpret_cast<float*>(misc + 4);  // [warps] largest normaliser
+        float* l_max = reinterpret_cast<float*>(misc + 4);  // [wg or half][4] largest normaliser
         float2* const all_rows = reinterpret_cast<float2*>(smem + C::OFF_ROW);
         int2* const all_limits = reinterpret_cast<int2*>(smem + C::OFF_LIM);
         int* const all_next = reinterpret_cast<int*>(smem + C::OFF_TOP);
@@ -1113,11 +1113,15 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                         }
                         if (lane < RW) atomicMax(next_ref + R0 + lane, ordered(top));
                         if (far && t > t0) {
-                            float x = 0.f;
 #pragma unroll
-                            for (int r = 0; r < RW; ++r) x = fmaxf(x, l[r]);
-                            x = warp_max(x);
-                            if (lane == 0) l_max[warp] = x;
+                            for (int j = 0; j < NH; ++j) {
+                                float x = 0.f;
+#pragma unroll
+                                for (int r = 0; r < RW; ++r)
+                                    if (half_of(r) == j) x = fmaxf(x, l[r]);
+                                x = warp_max(x);
+                                if (lane == 0) l_max[j * 4 + warp] = x;
+                            }
                         }
                     }
                     // V rows that no query sees may hold any code: a weight of 0 times NaN
@@ -1159,7 +1163,7 @@ __global__ void __launch_bounds__(Kv8Cfg<ROWS>::THREADS, Kv8Cfg<ROWS>::CTAS_PER_
                         ratio[j] = v[j] > 0.f ? v0 / v[j] : 0.f;
                         fall[j] = t > t0 && vref[j] > v0 ? __log2f(v[j]) - vrun[half0 + j].y : 0.f;
                         if (far && t > t0) {  // no further than the normaliser has room
-                            const float* x = l_max + wg * 4;
+                            const float* x = l_max + (wg + j) * 4;
                             const float most = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
                             fall[j] = fminf(fminf(fall[j], 1000.f),
                                             fmaxf(-kFar - __log2f(most), 0.f));

@@ -172,6 +172,22 @@ def test_coarse_block_and_drafted_tokens(Hkv, G_, D, n, window, e):
         attend(coarse_block(1500, Hkv, G_, D, e, 50, seed=e + n), B, n=n, window=window)
 
 
+@pytest.mark.parametrize("Hkv,G_,n", [(2, 1, 1), (2, 3, 1), (3, 1, 3), (2, 8, 1), (2, 9, 2)])
+@pytest.mark.parametrize("e", [20, 60])
+def test_coarse_blocks_of_neighbouring_heads_one_after_the_other(Hkv, G_, n, e):
+    """Heads of 64 dimensions that share a tile's rows of 128 bytes: when the second one meets
+    its coarse block, the first one's references have fallen already."""
+    L = 2000
+    z = normal((Hkv, G_, L), e, 0.3)
+    v_exp = torch.zeros(-(-L // BLOCK), Hkv, device=DEV)
+    for h in range(Hkv):
+        at = 20 + 40 * h
+        v_exp[at, h] = e
+        z[h, :, at * BLOCK:at * BLOCK + BLOCK] = -(e * math.log(2) + 30)
+    for B in (1, 300):
+        attend(Sequence(z, values(L, Hkv, 64, e), v_exp, e + 1), B, n=n)
+
+
 def steps(L, D, up, down, order, seed):
     """Tiles of 128 keys whose scales grow by 2^up from each to the next while their logits fall
     by `down` bits (or the other way round): every head has its weight where p * scale is."""
